@@ -82,9 +82,15 @@ typedef enum sk_status {
     SK_ERR_CAPTURE = 15,       /* a host-synchronous call (a stop rule, sk_fs2_solve) on a
                                   stream under graph capture */
     SK_ERR_LR = 16,            /* the gradient-flow step size is not finite */
-    SK_ERR_SCRATCH = 17        /* sk_solve_noalloc: sk_workspace_bytes(n, m, d) exceeds
+    SK_ERR_SCRATCH = 17,       /* sk_solve_noalloc: sk_workspace_bytes(n, m, d) exceeds
                                   SK_NOALLOC_SCRATCH_BYTES */
+    SK_ERR_DTYPE = 18,         /* unknown element type, or an address not aligned to its elements */
+    SK_ERR_ROUTE = 19,         /* a routing option out of range (see sk_scores_route) */
+    SK_ERR_OVERLAP = 20        /* a gradient that overlaps the scores without taking their place */
 } sk_status;
+
+/* Element types of a score matrix. */
+typedef enum sk_dtype { SK_F32 = 0, SK_BF16 = 1, SK_F16 = 2 } sk_dtype;
 
 /* Bytes of the static device scratch that sk_solve_noalloc works in (64 MiB). */
 #define SK_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
@@ -442,6 +448,122 @@ int sk_fs2_solve(const float *x, const float *y, const float *a, const float *b,
                  float *f, float *g, int32_t *info_i, float *info_f,
                  int32_t *perm_x, int32_t *perm_y,
                  void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * ----- Operators on a given score matrix -------------------------------------
+ *
+ * The entry points above form their scores from point clouds.  Those below take
+ * scores that a model hands over: a router's tokens x experts, a head's rows x
+ * vocabulary.  `scores` is row-major, n rows of m scores with a row stride of
+ * ld >= m elements, of type sk_dtype, aligned to its elements (any address and
+ * stride otherwise; rows on 16-byte boundaries read fastest).  Scores and
+ * gradients may be 32 or 16 bits wide; every maximum, sum and exponential is
+ * float32 (float64 where noted), and all other arrays are contiguous.
+ *
+ * A score of -inf is masked: it has probability zero.  A row that the mask
+ * leaves empty gives the finite or infinite values stated with each entry
+ * point, never NaN.  A NaN or +inf score makes the floating outputs of its row
+ * NaN; indices stay valid and distinct, a NaN ranking as -inf.  Ties rank by
+ * the lower index.  Results are deterministic.  All calls enqueue only
+ * (capturable); a workspace may be shared by calls that are ordered in one stream,
+ * not by graphs or streams that run at the same time.
+ */
+
+/* Workspace bytes of sk_scores_solve (0 for invalid sizes): n >= 1, 1 <= m <= 1024. */
+size_t sk_scores_solve_workspace_bytes(int64_t n, int64_t m);
+
+/*
+ * Sinkhorn potentials of a score matrix: the half-steps of sk_solve with the
+ * cost C = -scores, n_iters iterations from g_init (m floats, or NULL for 0; it
+ * may alias g):
+ *     f_i <- -eps * LSE_j[(g_j + s_ij)/eps + log b_j],
+ *     g_j <- -eps * LSE_i[(f_i + s_ij)/eps + log a_i].
+ * a (n) and b (m) are weights of equal mass, used as given; NULL means uniform
+ * 1/n, 1/m.  For a router, rows are tokens (weight 0 for padding, whose scores
+ * are then not looked at) and columns experts (b their capacities); with b
+ * uniform, g is the bias under which the plan a_i b_j exp((f_i + g_j + s_ij)/eps)
+ * loads the experts evenly: pass it to sk_scores_route with select_on = 1.
+ * Each iteration reads the scores once and takes one exponential per score.
+ * A row or column without any unmasked score of positive weight gets potential
+ * 0; so does one whose s/eps all lies below the float32 range.  Scores that are +inf or
+ * NaN in a row of positive weight make the potentials NaN.
+ */
+int sk_scores_solve(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,
+                    const float *a, const float *b, float eps, int32_t n_iters,
+                    const float *g_init, float *f, float *g,
+                    void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Routing: the k experts of every row and their weights.  m <= 1024, n >= 0.
+ * act_ij = softmax_j(s_i.) (score_fn 0) or sigmoid(s_ij) (score_fn 1).  The
+ * choice is by v_ij = (act_ij, or s_ij with select_on = 1) + bias_j (bias: m
+ * floats or NULL).  With n_group > 1 (a divisor of m, <= 64) only the topk_group
+ * best groups of m / n_group neighbouring columns take part, a group's score
+ * being the sum of its group_top (1 or 2) largest v.  idx (n, k) receives the
+ * k <= 64 largest v in descending order, ties by the lower index; the order
+ * is that of the definition (values closer than float32 can tell apart are
+ * taken in float64).  weights (n, k) are act at idx, without the bias, divided by
+ * their sum with renorm = 1 (exact also where act underflows), times scale; a
+ * chosen expert that is masked has weight 0.  counts (m, or NULL) receives how many rows
+ * chose each expert.  Options out of range return SK_ERR_ROUTE.
+ */
+int sk_scores_route(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,
+                    int32_t score_fn, const float *bias, int32_t select_on,
+                    int32_t n_group, int32_t topk_group, int32_t group_top,
+                    int32_t k, int32_t renorm, float scale,
+                    int32_t *idx, float *weights, int32_t *counts, void *stream);
+
+/*
+ * Gradient of sk_scores_route's weights in the scores, for the choice idx
+ * (n, k) held fixed: grad (n rows of m, stride ld_grad, the scores' type) from
+ * d_weights (n, k).  The bias takes part in the choice only and has no
+ * gradient.  Entries of idx outside [0, m) were dropped and have no part; an index
+ * that stands twice counts twice.  grad may be scores itself (same stride), and
+ * must not overlap it otherwise.
+ */
+int sk_scores_route_grad(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,
+                         int32_t score_fn, const int32_t *idx, const float *d_weights,
+                         int32_t k, int32_t renorm, float scale,
+                         void *grad, int64_t ld_grad, void *stream);
+
+/* Workspace bytes of sk_scores_logprobs (0 for invalid arguments). */
+size_t sk_scores_logprobs_workspace_bytes(int32_t dtype, int64_t n, int64_t m, int32_t top);
+
+/*
+ * Log-probabilities under p_i = softmax(s_i. / eps) (eps: the temperature),
+ * n >= 0 rows in one read of the scores:
+ *     lse[i]     = log sum_j exp(s_ij / eps),
+ *     logp[i]    = log p_i[targets[i]]; 0 for a target < 0 (no token given), NaN
+ *                  for one >= m (targets: n int64, or NULL with logp unused),
+ *     entropy[i] = -sum_j p_ij log p_ij (or NULL: not computed),
+ *     top_idx, top_logp (n, top): the top <= min(m, 64) largest, in descending
+ *                  order, with their log-probabilities (m <= 2^20 if top > 0),
+ *     stats (n, 2): max_j s_ij and log sum_j exp((s_ij - max)/eps), what the
+ *                  gradient needs of the row.
+ * An empty row has lse = -inf, log-probabilities -inf, entropy 0.
+ */
+int sk_scores_logprobs(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,
+                       float eps, const int64_t *targets, int32_t top,
+                       float *logp, float *lse, float *entropy,
+                       int32_t *top_idx, float *top_logp, float *stats,
+                       void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of sk_scores_logprobs in the scores,
+ *     grad_ij = (1/eps) { p_ij [ d_lse_i - d_logp_i - sum_r d_top_ir
+ *                                - d_entropy_i (log p_ij + entropy_i) ]
+ *                         + d_logp_i [j = targets_i] + sum_r d_top_ir [j = top_idx_ir] },
+ * from the forward's stats, entropy (needed with d_entropy) and top_idx (needed
+ * with d_top); each d_* may be NULL (zero).  A target < 0 takes no part, nor does a top_idx
+ * outside [0, m); equal picks add up.  grad (stride ld_grad, the scores' type) may be scores
+ * itself (same stride), and must not overlap it otherwise.  The gradient of an
+ * empty row is that of its picks alone.
+ */
+int sk_scores_logprobs_grad(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,
+                            float eps, const int64_t *targets, const float *stats,
+                            const float *entropy, int32_t top, const int32_t *top_idx,
+                            const float *d_logp, const float *d_lse, const float *d_entropy,
+                            const float *d_top, void *grad, int64_t ld_grad, void *stream);
 
 /*
  * Kernel timing of the streamed log-sum-exp passes (benchmark diagnostics).

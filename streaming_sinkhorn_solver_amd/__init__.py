@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -30,13 +31,19 @@ _STATUS_NAMES = {
     5: "SK_ERR_ITERS", 6: "SK_ERR_CHECK_EVERY", 7: "SK_ERR_NEG_WEIGHT", 8: "SK_ERR_MASS_MISMATCH",
     9: "SK_ERR_EMPTY_MEASURE", 10: "SK_ERR_NONFINITE", 11: "SK_ERR_WORKSPACE", 12: "SK_ERR_HIP",
     13: "SK_ERR_VARIANT", 14: "SK_ERR_STOP", 15: "SK_ERR_CAPTURE", 16: "SK_ERR_LR", 17: "SK_ERR_SCRATCH",
+    18: "SK_ERR_DTYPE", 19: "SK_ERR_ROUTE", 20: "SK_ERR_OVERLAP",
 }
-_VALUE_ERRORS = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 13, 14, 15, 16, 17}
+_VALUE_ERRORS = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 13, 14, 15, 16, 17, 18, 19, 20}
 NOALLOC_SCRATCH_BYTES = 64 << 20  # SK_NOALLOC_SCRATCH_BYTES of include/sk.h
 
 # SinkSLOT README, API Reference: variant and stop_mode names
 VARIANTS = {"alternating": 0, "symmetric": 1}
 STOP_MODES = {"fixed": 0, "marginal": 1, "potential": 2}
+
+# operators on a given score matrix: element types (sk_dtype), score functions and where the choice is made
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+SCORE_FNS = {"softmax": 0, "sigmoid": 1}
+SELECT_ON = {"score": 0, "logit": 1}
 
 # C ABI: (name, restype, argtypes)
 _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -74,6 +81,18 @@ SIGNATURES = {
     "sk_fs2_solve": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _f32, _i32, _f32, _f32, _i32, _i32, _f32,
                                     _i32, _i32, _i32, _i32, _vp, _vp, ctypes.POINTER(_i32), ctypes.POINTER(_f32), _vp,
                                     _vp, _vp, _sz, _vp]),
+    "sk_scores_solve_workspace_bytes": (_sz, [_i64, _i64]),
+    "sk_scores_solve": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _f32, _i32, _vp, _vp, _vp, _vp, _sz,
+                                       _vp]),
+    "sk_scores_route": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                       _f32, _vp, _vp, _vp, _vp]),
+    "sk_scores_route_grad": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _i32, _f32, _vp, _i64,
+                                            _vp]),
+    "sk_scores_logprobs_workspace_bytes": (_sz, [_i32, _i64, _i64, _i32]),
+    "sk_scores_logprobs": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _vp, _sz, _vp]),
+    "sk_scores_logprobs_grad": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
+                                               _vp, _vp, _vp, _i64, _vp]),
     "sk_timing_enable": (ctypes.c_int, [ctypes.c_int]),
     "sk_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64),
                                       ctypes.POINTER(ctypes.c_double)]),
@@ -534,6 +553,217 @@ def grad_x(x, y, a, b, g, *, eps: float, ws: torch.Tensor | None = None,
     return out
 
 
+def _scores(scores):
+    """A score matrix as (tensor, dtype code, n, m, row stride): (n, m) float32, bfloat16 or float16 on a GPU, any
+    row stride; scores whose neighbours in a row do not lie next to each other are copied."""
+    if not isinstance(scores, torch.Tensor):
+        raise TypeError("scores must be a torch tensor")
+    code = DTYPES.get(scores.dtype)
+    if code is None:
+        raise ValueError(f"scores must be float32, bfloat16 or float16 (got {scores.dtype})")
+    if scores.dim() != 2:
+        raise ValueError(f"scores must be (n, m) (got shape {tuple(scores.shape)})")
+    if scores.device.type != "cuda":
+        raise ValueError("scores must be on a GPU device")
+    n, m = scores.shape
+    ld = scores.stride(0)
+    if (m > 1 and scores.stride(1) != 1) or (n > 1 and ld < m):
+        scores = scores.contiguous()
+        ld = m
+    return scores, code, n, m, max(ld, m)
+
+
+def _grad_buf(grad, scores):
+    """The gradient of a score matrix: a caller's (n, m) tensor of its type with contiguous rows, or a new one."""
+    if grad is None:
+        return torch.empty(scores.shape, dtype=scores.dtype, device=scores.device)
+    n, m = scores.shape
+    if not isinstance(grad, torch.Tensor) or grad.dtype != scores.dtype or grad.device != scores.device:
+        raise ValueError(f"grad must be a {scores.dtype} tensor on {scores.device}")
+    if grad.shape != scores.shape or (m > 1 and grad.stride(1) != 1) or (n > 1 and grad.stride(0) < m):
+        raise ValueError(f"grad must be ({n}, {m}) with contiguous rows (got {tuple(grad.shape)})")
+    return grad
+
+
+def _vec(t, n, dtype, device, name):
+    """An optional (n,) input (or of shape n, a tuple), contiguous."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+    if tuple(t.shape) != (n if isinstance(n, tuple) else (n,)):
+        raise ValueError(f"{name} must have shape {n if isinstance(n, tuple) else (n,)} (got {tuple(t.shape)})")
+    return t.contiguous()
+
+
+def _call(name: str, device, *args):
+    """Calls an entry point on the scores' device and its current stream (the last argument)."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, _stream(device))
+    if code:
+        _raise(code, name)
+
+
+def scores_solve_workspace(n: int, m: int, device) -> torch.Tensor:
+    """A workspace tensor for scores_solve on an (n, m) score matrix."""
+    nb = int(load_library().sk_scores_solve_workspace_bytes(n, m))
+    if nb == 0:
+        raise ValueError(f"invalid problem size n={n} m={m} (n >= 1, 1 <= m <= 1024)")
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def scores_solve(scores, a=None, b=None, *, eps: float, n_iters: int, g_init: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None, f: torch.Tensor | None = None, g: torch.Tensor | None = None,
+                 check: bool = True):
+    """Sinkhorn potentials (f (n,), g (m,)) of a given score matrix (cost -scores), from g_init or 0.
+
+    For a router, rows are tokens (a: zero for padding) and columns experts (b: their capacities); a and b default
+    to uniform weights.  g (plus eps * log b where b is not uniform) is the bias for balance that ``scores_route``
+    takes with select_on="logit".  g_init may be g itself.  With check, given weights are validated as in
+    ``check_inputs`` (this waits for the stream)."""
+    s, code, n, m, ld = _scores(scores)
+    a, b = _vec(a, n, torch.float32, s.device, "a"), _vec(b, m, torch.float32, s.device, "b")
+    if check and (a is not None or b is not None):
+        aa = torch.full((n,), 1.0 / n, dtype=torch.float32, device=s.device) if a is None else a
+        bb = torch.full((m,), 1.0 / m, dtype=torch.float32, device=s.device) if b is None else b
+        with torch.cuda.device(s.device):
+            check_inputs(aa[:, None], bb[:, None], aa, bb)
+    g_init = _vec(g_init, m, torch.float32, s.device, "g_init")
+    ws = _ws(ws, s.device, lambda: scores_solve_workspace(n, m, s.device))
+    f = _buf(f, (n,), torch.float32, s.device, "f")
+    g = _buf(g, (m,), torch.float32, s.device, "g")
+    _call("sk_scores_solve", s.device, s.data_ptr(), code, n, m, ld, _ptr(a), _ptr(b), float(eps), int(n_iters),
+          _ptr(g_init), _ptr(f), _ptr(g), _ptr(ws), ws.numel())
+    return f, g
+
+
+class Routing(NamedTuple):
+    """Chosen experts (n, k) int32, their weights (n, k) float32, and rows per expert (m,) int32 or None."""
+    idx: torch.Tensor
+    weights: torch.Tensor
+    counts: torch.Tensor | None
+
+
+def scores_route(scores, k: int, *, score_fn: str = "softmax", bias: torch.Tensor | None = None,
+                 select_on: str = "score", n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+                 renorm: bool = True, scale: float = 1.0, counts: bool = False,
+                 out: Routing | None = None) -> Routing:
+    """The k experts of every row of a score matrix and their weights.
+
+    The choice is by softmax or sigmoid of the scores (select_on="score"), or by the scores themselves ("logit"),
+    plus bias (m,); with n_group > 1 inside the topk_group best groups of columns (by the sum of a group's group_top
+    largest values).  The weights are the softmax or sigmoid at the choice, divided by their sum with renorm, times
+    scale.  ``out``: a Routing of earlier buffers to write into."""
+    if score_fn not in SCORE_FNS or select_on not in SELECT_ON:
+        raise ValueError(f"score_fn must be one of {list(SCORE_FNS)}, select_on one of {list(SELECT_ON)}")
+    s, code, n, m, ld = _scores(scores)
+    k = int(k)
+    if not 1 <= k <= m:
+        raise ValueError(f"k must be between 1 and the {m} columns (got {k})")
+    bias = _vec(bias, m, torch.float32, s.device, "bias")
+    idx = _buf(out.idx if out else None, (n, k), torch.int32, s.device, "out.idx")
+    weights = _buf(out.weights if out else None, (n, k), torch.float32, s.device, "out.weights")
+    cnt = _buf(out.counts if out else None, (m,), torch.int32, s.device, "out.counts") if counts else None
+    _call("sk_scores_route", s.device, s.data_ptr(), code, n, m, ld, SCORE_FNS[score_fn], _ptr(bias),
+          SELECT_ON[select_on], int(n_group), int(topk_group), int(group_top), k, int(bool(renorm)), float(scale),
+          idx.data_ptr(), weights.data_ptr(), _ptr(cnt))
+    return Routing(idx, weights, cnt)
+
+
+def scores_route_grad(scores, idx, d_weights, *, score_fn: str = "softmax", renorm: bool = True, scale: float = 1.0,
+                      grad: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of ``scores_route``'s weights in the scores, for the choice idx (n, k) held fixed; grad may be scores
+    itself."""
+    if score_fn not in SCORE_FNS:
+        raise ValueError(f"score_fn must be one of {list(SCORE_FNS)}")
+    s, code, n, m, ld = _scores(scores)
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or idx.shape[0] != n:
+        raise ValueError(f"idx must be an ({n}, k) int32 tensor")
+    k = idx.shape[1]
+    idx = _vec(idx, (n, k), torch.int32, s.device, "idx")
+    d_weights = _vec(d_weights, (n, k), torch.float32, s.device, "d_weights")
+    if d_weights is None:
+        raise ValueError("d_weights must be given")
+    grad = _grad_buf(grad, s)
+    _call("sk_scores_route_grad", s.device, s.data_ptr(), code, n, m, ld, SCORE_FNS[score_fn], idx.data_ptr(),
+          d_weights.data_ptr(), k, int(bool(renorm)), float(scale), grad.data_ptr(), max(grad.stride(0), m))
+    return grad
+
+
+class Logprobs(NamedTuple):
+    """Of each row: log-probability of its target (or None), log-sum-exp, entropy (or None), the largest entries'
+    columns and log-probabilities (or None), and (maximum, log sum) for the gradient."""
+    logp: torch.Tensor | None
+    lse: torch.Tensor
+    entropy: torch.Tensor | None
+    top_idx: torch.Tensor | None
+    top_logp: torch.Tensor | None
+    stats: torch.Tensor
+
+
+def scores_logprobs_workspace(dtype: torch.dtype, n: int, m: int, top: int, device) -> torch.Tensor:
+    """A workspace tensor for scores_logprobs on an (n, m) score matrix of this dtype."""
+    nb = int(load_library().sk_scores_logprobs_workspace_bytes(DTYPES.get(dtype, -1), n, m, top))
+    if nb == 0:
+        raise ValueError(f"invalid arguments for scores_logprobs (dtype={dtype} n={n} m={m} top={top}: top <= 64, "
+                         "top <= m, and m <= 2**20 where top > 0)")
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def scores_logprobs(scores, targets: torch.Tensor | None = None, *, eps: float = 1.0, top: int = 0,
+                    entropy: bool = False, ws: torch.Tensor | None = None, out: Logprobs | None = None) -> Logprobs:
+    """Log-probabilities of targets (n,) int64 (negative: no token given) under softmax(scores / eps), with the rows'
+    log-sum-exp, their entropy and the ``top`` largest alternatives, in one read of the scores.  ``out``: a Logprobs
+    of earlier buffers to write into."""
+    s, code, n, m, ld = _scores(scores)
+    top = int(top)
+    dev = s.device
+    targets = _vec(targets, n, torch.int64, dev, "targets")
+    ws = _ws(ws, dev, lambda: scores_logprobs_workspace(s.dtype, n, m, top, dev))
+    logp = None if targets is None else _buf(out.logp if out else None, (n,), torch.float32, dev, "out.logp")
+    lse = _buf(out.lse if out else None, (n,), torch.float32, dev, "out.lse")
+    ent = _buf(out.entropy if out else None, (n,), torch.float32, dev, "out.entropy") if entropy else None
+    top_idx = _buf(out.top_idx if out else None, (n, top), torch.int32, dev, "out.top_idx") if top > 0 else None
+    top_logp = _buf(out.top_logp if out else None, (n, top), torch.float32, dev, "out.top_logp") if top > 0 else None
+    stats = _buf(out.stats if out else None, (n, 2), torch.float32, dev, "out.stats")
+    _call("sk_scores_logprobs", dev, s.data_ptr(), code, n, m, ld, float(eps), _ptr(targets), top, _ptr(logp),
+          lse.data_ptr(), _ptr(ent), _ptr(top_idx), _ptr(top_logp), stats.data_ptr(), ws.data_ptr(), ws.numel())
+    return Logprobs(logp, lse, ent, top_idx, top_logp, stats)
+
+
+def scores_logprobs_grad(scores, targets: torch.Tensor | None, fwd: Logprobs, *, eps: float = 1.0,
+                         d_logp: torch.Tensor | None = None, d_lse: torch.Tensor | None = None,
+                         d_entropy: torch.Tensor | None = None, d_top: torch.Tensor | None = None,
+                         grad: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of ``scores_logprobs`` in the scores from the gradients of its outputs (each optional; d_top is that
+    of top_logp); fwd is its result for the same scores, targets and eps.  grad may be scores itself."""
+    s, code, n, m, ld = _scores(scores)
+    dev = s.device
+    targets = _vec(targets, n, torch.int64, dev, "targets")
+    stats = _in(fwd.stats, (n, 2), dev, "fwd.stats")
+    if d_logp is not None and targets is None:
+        raise ValueError("d_logp needs targets")
+    if d_entropy is not None and fwd.entropy is None:
+        raise ValueError("d_entropy needs the forward's entropy")
+    if d_top is not None and fwd.top_idx is None:
+        raise ValueError("d_top needs the forward's top_idx")
+    top = 0 if d_top is None else fwd.top_idx.shape[1]
+    ent = None if d_entropy is None else _vec(fwd.entropy, n, torch.float32, dev, "fwd.entropy")
+    top_idx = None if d_top is None else _vec(fwd.top_idx, (n, top), torch.int32, dev, "fwd.top_idx")
+    d_logp, d_lse = _vec(d_logp, n, torch.float32, dev, "d_logp"), _vec(d_lse, n, torch.float32, dev, "d_lse")
+    d_entropy = _vec(d_entropy, n, torch.float32, dev, "d_entropy")
+    d_top = _vec(d_top, (n, top), torch.float32, dev, "d_top")
+    grad = _grad_buf(grad, s)
+    _call("sk_scores_logprobs_grad", dev, s.data_ptr(), code, n, m, ld, float(eps), _ptr(targets), stats.data_ptr(),
+          _ptr(ent), top, _ptr(top_idx), _ptr(d_logp), _ptr(d_lse), _ptr(d_entropy), _ptr(d_top), grad.data_ptr(),
+          max(grad.stride(0), m))
+    return grad
+
+
 def timing_enable(enable: bool = True, stride: int = 1) -> None:
     """Start (reset) or stop event timing of the streamed-pass kernels; every
     stride-th pass launch is timed."""
@@ -553,4 +783,6 @@ __all__ = ["timing_enable", "timing_read", "solve", "solve_ex", "gradient_flow",
            "transport_workspace", "cost", "dual_cost", "divergence",
            "divergence_workspace", "marginal_residual", "grad_x", "check_inputs", "workspace", "workspace_bytes",
            "load_library", "status_string", "SinkhornError", "LIB_PATH", "SIGNATURES", "VARIANTS", "STOP_MODES",
-           "solve_noalloc", "NOALLOC_SCRATCH_BYTES", "solve_warm", "primal_cost"]
+           "solve_noalloc", "NOALLOC_SCRATCH_BYTES", "solve_warm", "primal_cost",
+           "scores_solve", "scores_solve_workspace", "scores_route", "scores_route_grad", "Routing", "scores_logprobs",
+           "scores_logprobs_grad", "scores_logprobs_workspace", "Logprobs", "DTYPES", "SCORE_FNS", "SELECT_ON"]

@@ -1404,6 +1404,11 @@ const char* sk_status_string(int status) {
         case SK_ERR_SCRATCH:
             return "the problem needs more workspace than the static scratch of sk_solve_noalloc holds "
                    "(sk_workspace_bytes(n, m, d) > SK_NOALLOC_SCRATCH_BYTES)";
+        case SK_ERR_DTYPE: return "unknown element type, or an address not aligned to its elements";
+        case SK_ERR_ROUTE:
+            return "a routing option is out of range (groups divide m, topk_group <= n_group, group_top 1 or 2, "
+                   "k <= 64 within the chosen groups)";
+        case SK_ERR_OVERLAP: return "the gradient overlaps the scores without taking their place";
         default: return "unknown status";
     }
 }
