@@ -52,9 +52,9 @@ inline int elem_size(int32_t dtype) { return dtype == SK_F32 ? 4 : 2; }
 __device__ __forceinline__ float s_ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float s_lg2(float x) { return __builtin_amdgcn_logf(x); }
 
-// ----- reductions over groups of L consecutive lanes (L = 8, 16 or 64), result in every lane --------
-// Inside a row of 16 lanes by rotations (L = 16) or half-row mirror and quad
-// permutations (L = 8); across the four rows of a wave by the row swaps.
+// ----- reductions over groups of L consecutive lanes (L = 4, 8, 16 or 64), result in every lane --------
+// Inside a row of 16 lanes by quad permutations, half-row mirror and rotation;
+// across the four rows of a wave by the row swaps.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t x) {
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);
@@ -62,14 +62,15 @@ __device__ __forceinline__ uint32_t dpp(uint32_t x) {
 constexpr int kQuadXor1 = 0xb1;     // quad_perm [1, 0, 3, 2]
 constexpr int kQuadXor2 = 0x4e;     // quad_perm [2, 3, 0, 1]
 constexpr int kHalfMirror = 0x141;  // row_half_mirror: lane i <- 7 - i in each 8 lanes
+constexpr int kRor4 = 0x124;        // row_ror:4
 constexpr int kRor8 = 0x128;        // row_ror:8
 
 template <int L, class Op>
 __device__ __forceinline__ uint32_t lanes_reduce(uint32_t x, Op op) {
-    static_assert(L == 8 || L == 16 || L == 64, "lanes per row");
+    static_assert(L == 4 || L == 8 || L == 16 || L == 64, "lanes per row");
     x = op(x, dpp<kQuadXor1>(x));
     x = op(x, dpp<kQuadXor2>(x));
-    x = op(x, dpp<kHalfMirror>(x));
+    if constexpr (L >= 8) x = op(x, dpp<kHalfMirror>(x));
     if constexpr (L >= 16) x = op(x, dpp<kRor8>(x));
     if constexpr (L == 64) {
         auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
@@ -97,6 +98,22 @@ struct OpMinU {
     __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; }
 };
 
+// Sum over the 64 / L groups of L lanes of a wave (lanes with the same number in their groups), in every lane.
+template <int L>
+__device__ __forceinline__ float groups_sum(float x) {
+    uint32_t u = __builtin_bit_cast(uint32_t, x);
+    OpAddF add;
+    if constexpr (L <= 8) u = add(u, dpp<kRor8>(u));
+    if constexpr (L <= 4) u = add(u, dpp<kRor4>(u));
+    if constexpr (L <= 16) {
+        auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        u = add((uint32_t)r[0], (uint32_t)r[1]);
+        r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        u = add((uint32_t)r[0], (uint32_t)r[1]);
+    }
+    return __builtin_bit_cast(float, u);
+}
+
 template <int L>
 __device__ __forceinline__ float lanes_max(float x) {
     return __builtin_bit_cast(float, lanes_reduce<L>(__builtin_bit_cast(uint32_t, x), OpMaxF()));
@@ -119,6 +136,47 @@ template <int L>
 __device__ __forceinline__ uint32_t lanes_min(uint32_t x) {
     return lanes_reduce<L>(x, OpMinU());
 }
+
+// ----- a row in the registers of L lanes, E scores per lane -------------------------------
+// With V the lane takes runs of W neighbouring scores (16 bytes at most) from
+// rows whose runs are aligned and whose m is a multiple of W; without, single
+// scores L apart, from any row.
+template <class T, int L, int E, bool V>
+struct Row {
+    using Elem = typename T::type;
+    static constexpr int kMost = 16 / (int)sizeof(Elem);
+    static constexpr int W = V ? (E < kMost ? E : kMost) : 1;
+    __device__ static int col(int e, int l) { return (e / W * L + l) * W + e % W; }
+    struct alignas(W * sizeof(Elem)) Run {
+        Elem v[W];
+    };
+    // fetch only issues the loads; get converts what arrived (MASK: -inf behind the row, else some score of it).
+    struct Raw {
+        Run r[E / W];
+    };
+    __device__ static void fetch(const Elem* row, int l, int m, Raw& raw) {
+#pragma unroll
+        for (int q = 0; q < E / W; ++q) {
+            const int j = col(q * W, l);
+            raw.r[q] = *reinterpret_cast<const Run*>(row + (j < m ? j : W == 1 ? m - 1 : 0));
+        }
+    }
+    template <bool MASK = true>
+    __device__ static void get(const Raw& raw, int l, int m, float (&s)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            s[e] = !MASK || col(e / W * W, l) < m ? T::to(raw.r[e / W].v[e % W]) : -INFINITY;
+    }
+    __device__ static void load(const Elem* row, int l, int m, float (&s)[E]) {
+        Raw raw;
+        fetch(row, l, m, raw);
+        get(raw, l, m, s);
+    }
+    // Whether the rows of a matrix can be read in runs.
+    static bool fits(const void* p, int64_t ld, int64_t m) {
+        return W > 1 && m % W == 0 && ld % W == 0 && reinterpret_cast<uintptr_t>(p) % (W * sizeof(Elem)) == 0;
+    }
+};
 
 // LDS written by this wave's lanes is visible to its other lanes (one wave's
 // LDS operations complete in order; this stops the compiler from moving them).

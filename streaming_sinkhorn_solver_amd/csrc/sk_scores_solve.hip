@@ -15,6 +15,15 @@
 // small to be sure of it (or whose b_j is zero) takes its log-sum-exp over the
 // rows directly.  Sums over rows run in a fixed order (per lane, lanes, waves,
 // workgroups): results are deterministic.
+//
+// An iteration is two launches: the pass leaves each workgroup's column sums,
+// the update joins them.  At 32768 x 256 bfloat16 an iteration takes 8.9 us: 6.6
+// the pass (16.8 MB from the caches in 2 row steps per wave, about 3 us of
+// instruction issue; the rest is latency: launch, column terms, first rows, joining in LDS)
+// and 2.3 the update.  Problems of at most 32 scores per thread of one workgroup
+// run all their iterations in a single launch: 8 iterations of 200 x 16 take 12 us
+// against 40 in two launches each, and at the limit 30 against 43 (2048 x 16), 28
+// against 47 (512 x 64), 30 against 56 (128 x 256).
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -23,7 +32,9 @@ namespace sk {
 namespace {
 
 constexpr int kSolveMaxCols = 1024;
-constexpr int kSolveGroups = 512;  // workgroups of a pass: two per CU
+constexpr int kSolveThreads = 1024;  // of a pass: 16 waves, whose sums are joined in LDS before they reach memory
+constexpr int kSolveGroups = 256;    // workgroups of a pass: one per CU, so the update joins at most 256 partials
+constexpr int kSmallScores = 32;     // scores per thread of the single-workgroup kernel
 
 struct SolveArgs {
     const void* s;
@@ -35,52 +46,99 @@ struct SolveArgs {
     float* part;         // [groups][m] sums over each workgroup's rows
     float c, inv_c;      // log2e / eps, eps ln2
     int groups;
-    int last;
+    int last;            // the iteration is the last one
+    int iters;           // of the single-workgroup kernel
 };
 
-// One row per L lanes, E scores per lane (column e L + l), 64 / L rows per wave.
-template <class T, int L, int E>
-__global__ __launch_bounds__(kBlock) void k_solve_pass(SolveArgs A) {
-    constexpr int kSlots = kBlock / L;  // rows of one workgroup at a time
-    __shared__ float red[kBlock / 64][L * E];
-    const int l = threadIdx.x % L, slot = threadIdx.x / L;
-    const float l2b = -s_lg2((float)A.m);
-    float h[E], acc[E];
-    int col[E];
+// The row half-step of a row held as t (scores in base 2 with the column
+// terms): t becomes 2^(t - M), and the row's potential and the factor a / S of
+// its share in the column sums are returned.  A row that the mask leaves empty has S = 0: its
+// potential is 0 and it sends nothing; nor does a row of weight zero, whatever
+// it holds.
+template <int L, int E>
+__device__ __forceinline__ float row_step(const SolveArgs& A, float (&t)[E], float w, float* f) {
+    float M = kNegBig;
+#pragma unroll
+    for (int e = 0; e < E; ++e) M = fmaxf(M, t[e]);
+    M = lanes_max<L>(M);
+    float S = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int j = e * L + l;
-        col[e] = j < A.m ? j : A.m - 1;  // loads of the padding lanes stay inside the row
-        const float g = A.g_in ? A.g_in[col[e]] : 0.0f;
-        const float lb = A.b ? s_lg2(A.b[col[e]]) : l2b;
-        h[e] = j < A.m ? fmaf(g, A.c, lb) : -INFINITY;
+        t[e] = s_ex2(t[e] - M);
+        S += t[e];
+    }
+    S = lanes_sum<L>(S);
+    *f = S == 0.0f ? 0.0f : -A.inv_c * (M + s_lg2(S));
+    return S == 0.0f || w == 0.0f ? 0.0f : w * __builtin_amdgcn_rcpf(S);
+}
+
+__device__ __forceinline__ float log2_b(const SolveArgs& A, int j) { return A.b ? s_lg2(A.b[j]) : -s_lg2((float)A.m); }
+
+// Whether the sum c_j is sure to hold what its n terms add up to: each loses at
+// most 2^-126 to the exponential's flush, so above n 2^-100 less than a rounding is lost.
+__device__ __forceinline__ bool safe(const SolveArgs& A, float cj) { return cj >= (float)A.n * 0x1p-100f; }
+
+// The column half-step of one column by its log-sum-exp over the rows, by the whole workgroup.
+template <class T, int THREADS>
+__device__ float column_direct(const SolveArgs& A, int col, const float* f) {
+    __shared__ float wave_m[THREADS / 64], wave_s[THREADS / 64];
+    const float l2n = -s_lg2((float)A.n);
+    float M = kNegBig, S = 0.0f;
+    for (int64_t i = threadIdx.x; i < A.n; i += THREADS) {
+        if (A.a && A.a[i] == 0.0f) continue;
+        const float s = T::to(static_cast<const typename T::type*>(A.s)[i * A.ld + col]);
+        const float t = fmaf(s + f[i], A.c, A.a ? s_lg2(A.a[i]) : l2n);
+        const float top = fmaxf(M, t);
+        S = S * s_ex2(M - top) + s_ex2(t - top);
+        M = top;
+    }
+    const float top = lanes_max<64>(M);
+    const float s = lanes_sum<64>(S * s_ex2(M - top));
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) wave_m[threadIdx.x / 64] = top, wave_s[threadIdx.x / 64] = s;
+    __syncthreads();
+    float m2 = kNegBig, s2 = 0.0f;
+    for (int w = 0; w < THREADS / 64; ++w) m2 = fmaxf(m2, wave_m[w]);
+    for (int w = 0; w < THREADS / 64; ++w) s2 += wave_s[w] * s_ex2(wave_m[w] - m2);
+    return s2 == 0.0f ? 0.0f : -A.inv_c * (m2 + s_lg2(s2));
+}
+
+// One row per L lanes, E scores per lane, 1024 / L rows of a workgroup at a time.
+template <class T, int L, int E, bool V>
+__global__ __launch_bounds__(kSolveThreads) void k_solve_pass(SolveArgs A) {
+    constexpr int kSlots = kSolveThreads / L, kWaves = kSolveThreads / 64;
+    using R = Row<T, L, E, V>;
+    __shared__ float red[kWaves][L * E];
+    const int l = threadIdx.x % L, slot = threadIdx.x / L;
+    const float uniform = 1.0f / (float)A.n;
+    const int64_t step = (int64_t)A.groups * kSlots;
+    int64_t i = (int64_t)blockIdx.x * kSlots + slot;
+    typename R::Raw next;  // the next row, loaded while this one is worked on
+    auto fetch = [&](int64_t row) {
+        R::fetch(static_cast<const typename T::type*>(A.s) + (row < A.n ? row : 0) * A.ld, l, A.m, next);
+    };
+    fetch(i);
+    // the columns' terms, each loaded once and passed on through LDS
+    for (int j = threadIdx.x; j < L * E; j += kSolveThreads)
+        red[0][j] = j < A.m ? fmaf(A.g_in ? A.g_in[j] : 0.0f, A.c, log2_b(A, j)) : -INFINITY;
+    __syncthreads();
+    float h[E], acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        h[e] = red[0][R::col(e, l)];
         acc[e] = 0.0f;
     }
-    const float uniform = 1.0f / (float)A.n;
-    for (int64_t i0 = (int64_t)blockIdx.x * kSlots; i0 < A.n; i0 += (int64_t)A.groups * kSlots) {
-        const int64_t i = i0 + slot;
+    __syncthreads();
+    for (int64_t i0 = (int64_t)blockIdx.x * kSlots; i0 < A.n; i0 += step, i += step) {
         const bool on = i < A.n;
-        const typename T::type* row = static_cast<const typename T::type*>(A.s) + (on ? i : 0) * A.ld;
-        float t[E];
-        float M = kNegBig;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            t[e] = fmaf(T::to(row[col[e]]), A.c, h[e]);
-            M = fmaxf(M, t[e]);
-        }
-        M = lanes_max<L>(M);
-        float S = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            t[e] = s_ex2(t[e] - M);
-            S += t[e];
-        }
-        S = lanes_sum<L>(S);
-        // a row that the mask leaves empty has S = 0: its potential is 0 and it sends nothing; nor does a row
-        // of weight zero, whatever it holds
+        float t[E], f;
+        R::template get<false>(next, l, A.m, t);  // (behind the row h is -inf)
+        if (i0 + step < A.n) fetch(i + step);
         const float w = on ? (A.a ? A.a[i] : uniform) : 0.0f;
-        const float scale = S == 0.0f || w == 0.0f ? 0.0f : w / S;
-        if (on && l == 0) A.f[i] = S == 0.0f ? 0.0f : -A.inv_c * (M + s_lg2(S));
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[e] = fmaf(t[e], A.c, h[e]);
+        const float scale = row_step<L, E>(A, t, w, &f);
+        if (on && l == 0) A.f[i] = f;
         if (scale != 0.0f) {
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = fmaf(t[e], scale, acc[e]);
@@ -89,43 +147,49 @@ __global__ __launch_bounds__(kBlock) void k_solve_pass(SolveArgs A) {
     // rows of the wave, then the waves
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        for (int o = L; o < 64; o *= 2) acc[e] += __shfl_xor(acc[e], o);
-        if ((threadIdx.x & 63) < L) red[threadIdx.x / 64][e * L + l] = acc[e];
+        acc[e] = groups_sum<L>(acc[e]);
+        if ((threadIdx.x & 63) < L) red[threadIdx.x / 64][R::col(e, l)] = acc[e];
     }
     __syncthreads();
-    for (int j = threadIdx.x; j < A.m; j += kBlock) {
+    for (int j = threadIdx.x; j < A.m; j += kSolveThreads) {
         float sum = 0.0f;
-        for (int w = 0; w < kBlock / 64; ++w) sum += red[w][j];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sum += red[w][j];
         A.part[(int64_t)blockIdx.x * A.m + j] = sum;
     }
 }
 
-// The column half-step from the passes' partial sums: 32 columns per workgroup, 8 slices of the partials.
+// The column half-step from the passes' partial sums: 8 columns per workgroup, 32 slices of the partials.
 template <class T>
 __global__ __launch_bounds__(kBlock) void k_solve_update(SolveArgs A) {
-    constexpr int kCols = 32, kSlices = kBlock / kCols;
+    constexpr int kCols = 8, kSlices = kBlock / kCols;
     __shared__ float sum[kSlices][kCols];
-    __shared__ float wave_m[kBlock / 64], wave_s[kBlock / 64];
     __shared__ int direct[kCols];
     const int x = threadIdx.x % kCols, y = threadIdx.x / kCols;
     const int j = blockIdx.x * kCols + x;
+    const int jc = j < A.m ? j : 0;
+    const float g = A.g_in ? A.g_in[jc] : 0.0f, lb = log2_b(A, jc);
     float part = 0.0f;
-    if (j < A.m)
-        for (int w = y; w < A.groups; w += kSlices) part += A.part[(int64_t)w * A.m + j];
+    if (j < A.m) {
+#pragma unroll
+        for (int k = 0; k < kSolveGroups / kSlices; ++k) {
+            const int w = k * kSlices + y;
+            const float p = A.part[(int64_t)min(w, A.groups - 1) * A.m + j];
+            part += w < A.groups ? p : 0.0f;
+        }
+    }
     sum[y][x] = part;
     __syncthreads();
     if (y == 0) {
         float cj = 0.0f;
+#pragma unroll
         for (int k = 0; k < kSlices; ++k) cj += sum[k][x];
         int need = 0;
         if (j < A.m) {
-            const float g = A.g_in ? A.g_in[j] : 0.0f;
-            const float bj = A.b ? A.b[j] : 1.0f / (float)A.m;
-            // each of the n terms loses at most 2^-126: above n 2^-100 that is below a rounding
-            if (bj > 0.0f && cj >= (float)A.n * 0x1p-100f)
-                A.g[j] = fmaf(A.inv_c, s_lg2(bj) - s_lg2(cj), g);
-            else if (bj == 0.0f && !A.last)
-                A.g[j] = g;  // enters no row before the last iteration
+            if (lb > -INFINITY && safe(A, cj))
+                A.g[j] = fmaf(A.inv_c, lb - s_lg2(cj), g);
+            else if (lb == -INFINITY && !A.last)
+                A.g[j] = g;  // a column of weight zero enters no row before the last iteration
             else
                 need = 1;
         }
@@ -135,28 +199,95 @@ __global__ __launch_bounds__(kBlock) void k_solve_update(SolveArgs A) {
     for (int k = 0; k < kCols; ++k) {
         if (!direct[k]) continue;  // the same for the whole workgroup
         const int col = blockIdx.x * kCols + k;
-        const float l2n = -s_lg2((float)A.n);
-        float M = kNegBig, S = 0.0f;
-        for (int64_t i = threadIdx.x; i < A.n; i += kBlock) {
-            if (A.a && A.a[i] == 0.0f) continue;
-            const float s = T::to(static_cast<const typename T::type*>(A.s)[i * A.ld + col]);
-            const float t = fmaf(s + A.f[i], A.c, A.a ? s_lg2(A.a[i]) : l2n);
-            const float top = fmaxf(M, t);
-            S = S * s_ex2(M - top) + s_ex2(t - top);
-            M = top;
-        }
-        const float top = lanes_max<64>(M);
-        const float s = lanes_sum<64>(S * s_ex2(M - top));
-        if (threadIdx.x % 64 == 0) wave_m[threadIdx.x / 64] = top, wave_s[threadIdx.x / 64] = s;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float m2 = kNegBig, s2 = 0.0f;
-            for (int w = 0; w < kBlock / 64; ++w) m2 = fmaxf(m2, wave_m[w]);
-            for (int w = 0; w < kBlock / 64; ++w) s2 += wave_s[w] * s_ex2(wave_m[w] - m2);
-            A.g[col] = s2 == 0.0f ? 0.0f : -A.inv_c * (m2 + s_lg2(s2));
-        }
-        __syncthreads();
+        const float g = column_direct<T, kBlock>(A, col, A.f);
+        if (threadIdx.x == 0) A.g[col] = g;
     }
+}
+
+// All iterations in one workgroup, the scores in registers (R rows per slot).
+template <class T, int L, int E, bool V>
+__global__ __launch_bounds__(kSolveThreads) void k_solve_small(SolveArgs A) {
+    constexpr int kSlots = kSolveThreads / L, kWaves = kSolveThreads / 64, R = kSmallScores / E;
+    using Rw = Row<T, L, E, V>;
+    __shared__ float red[kWaves][L * E];
+    __shared__ float g[L * E], fs[kSlots * R];
+    __shared__ int direct[2];  // of this iteration and the next one
+    const int l = threadIdx.x % L, slot = threadIdx.x / L;
+    float s[R][E], lb[E], w[R];
+    const float uniform = 1.0f / (float)A.n;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = r * kSlots + slot;
+        const bool on = i < A.n;
+        typename Rw::Raw raw;
+        Rw::fetch(static_cast<const typename T::type*>(A.s) + (int64_t)(on ? i : 0) * A.ld, l, A.m, raw);
+        Rw::template get<false>(raw, l, A.m, s[r]);  // (behind the row lb is -inf)
+        w[r] = on ? (A.a ? A.a[i] : uniform) : 0.0f;
+    }
+    const float b2 = (int)threadIdx.x < A.m ? log2_b(A, threadIdx.x) : -INFINITY;  // of this thread's column
+    if (threadIdx.x < L * E) {
+        g[threadIdx.x] = (int)threadIdx.x < A.m && A.g_in ? A.g_in[threadIdx.x] : 0.0f;
+        red[0][threadIdx.x] = b2;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) lb[e] = red[0][Rw::col(e, l)];
+    if (threadIdx.x < 2) direct[threadIdx.x] = 0;
+    for (int k = 0; k < A.iters; ++k) {
+        __syncthreads();
+        float h[E], acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            h[e] = fmaf(g[Rw::col(e, l)], A.c, lb[e]);
+            acc[e] = 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r * kSlots >= A.n) break;
+            float t[E], f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) t[e] = fmaf(s[r][e], A.c, h[e]);
+            const float scale = row_step<L, E>(A, t, w[r], &f);
+            if (l == 0) fs[r * kSlots + slot] = f;
+            if (scale != 0.0f) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(t[e], scale, acc[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            acc[e] = groups_sum<L>(acc[e]);
+            if ((threadIdx.x & 63) < L) red[threadIdx.x / 64][Rw::col(e, l)] = acc[e];
+        }
+        __syncthreads();
+        const int j = threadIdx.x;
+        const bool last = k + 1 == A.iters;
+        bool need = false;
+        // (every thread has read the last iteration's flag before this iteration's first barrier)
+        if (threadIdx.x == 0) direct[(k + 1) & 1] = 0;
+        if (j < A.m) {
+            float cj = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q) cj += red[q][j];
+            if (b2 > -INFINITY && safe(A, cj))
+                g[j] = fmaf(A.inv_c, b2 - s_lg2(cj), g[j]);
+            else
+                need = b2 > -INFINITY || last;
+            if (need) direct[k & 1] = 1;
+            red[0][j] = need ? 1.0f : 0.0f;
+        }
+        __syncthreads();
+        if (direct[k & 1]) {
+            for (int q = 0; q < A.m; ++q) {
+                if (red[0][q] == 0.0f) continue;
+                const float x = column_direct<T, kSolveThreads>(A, q, fs);
+                if (threadIdx.x == 0) g[q] = x;
+            }
+            __syncthreads();
+        }
+    }
+    if ((int)threadIdx.x < A.m) A.g[threadIdx.x] = g[threadIdx.x];
+    for (int i = threadIdx.x; i < A.n; i += kSolveThreads) A.f[i] = fs[i];
 }
 
 // n_iters = 0: f = 0, g = g_init or 0.
@@ -166,31 +297,32 @@ __global__ __launch_bounds__(kBlock) void k_solve_start(SolveArgs A) {
     if (i < A.m) A.g[i] = A.g_in ? A.g_in[i] : 0.0f;
 }
 
-int solve_rows_per_group(int m) { return m <= 256 ? kBlock / 16 : kBlock / 64; }
-
-int solve_groups(int64_t n, int64_t m) {
-    const int rows = solve_rows_per_group((int)m);
-    return (int)std::min<int64_t>((n + rows - 1) / rows, kSolveGroups);
+// f(lanes per row, scores per lane) for rows of m scores.  Every lane of a row
+// repeats the row's own work (reductions, reciprocal), so a row gets as few
+// lanes as hold it at 16 scores each or less.
+template <class F>
+void solve_width(int m, F f) {
+    using std::integral_constant;
+    if (m <= 16)
+        f(integral_constant<int, 4>(), integral_constant<int, 4>());
+    else if (m <= 32)
+        f(integral_constant<int, 4>(), integral_constant<int, 8>());
+    else if (m <= 64)
+        f(integral_constant<int, 8>(), integral_constant<int, 8>());
+    else if (m <= 128)
+        f(integral_constant<int, 16>(), integral_constant<int, 8>());
+    else if (m <= 256)
+        f(integral_constant<int, 16>(), integral_constant<int, 16>());
+    else if (m <= 512)
+        f(integral_constant<int, 64>(), integral_constant<int, 8>());
+    else
+        f(integral_constant<int, 64>(), integral_constant<int, 16>());
 }
 
-template <class T>
-hipError_t launch_solve_pass(const SolveArgs& A, hipStream_t s) {
-    const dim3 grid(A.groups), block(kBlock);
-    if (A.m <= 16)
-        hipLaunchKernelGGL((k_solve_pass<T, 16, 1>), grid, block, 0, s, A);
-    else if (A.m <= 32)
-        hipLaunchKernelGGL((k_solve_pass<T, 16, 2>), grid, block, 0, s, A);
-    else if (A.m <= 64)
-        hipLaunchKernelGGL((k_solve_pass<T, 16, 4>), grid, block, 0, s, A);
-    else if (A.m <= 128)
-        hipLaunchKernelGGL((k_solve_pass<T, 16, 8>), grid, block, 0, s, A);
-    else if (A.m <= 256)
-        hipLaunchKernelGGL((k_solve_pass<T, 16, 16>), grid, block, 0, s, A);
-    else if (A.m <= 512)
-        hipLaunchKernelGGL((k_solve_pass<T, 64, 8>), grid, block, 0, s, A);
-    else
-        hipLaunchKernelGGL((k_solve_pass<T, 64, 16>), grid, block, 0, s, A);
-    return hipGetLastError();
+int solve_groups(int64_t n, int64_t m) {
+    int64_t rows = 0;
+    solve_width((int)m, [&](auto lanes, auto) { rows = kSolveThreads / decltype(lanes)::value; });
+    return (int)std::min<int64_t>((n + rows - 1) / rows, kSolveGroups);
 }
 
 template <class T>
@@ -201,14 +333,31 @@ int solve(SolveArgs A, int n_iters, hipStream_t s) {
         SK_TRY_LAUNCH(hipGetLastError());
         return SK_OK;
     }
-    for (int k = 0; k < n_iters; ++k) {
-        A.last = k + 1 == n_iters;
-        SK_TRY_LAUNCH(launch_solve_pass<T>(A, s));
-        hipLaunchKernelGGL((k_solve_update<T>), dim3((unsigned)((A.m + 31) / 32)), dim3(kBlock), 0, s, A);
-        SK_TRY_LAUNCH(hipGetLastError());
-        A.g_in = A.g;
-    }
-    return SK_OK;
+    int st = SK_OK;
+    solve_width(A.m, [&](auto lanes, auto per_lane) {
+        constexpr int L = decltype(lanes)::value, E = decltype(per_lane)::value;
+        auto small = k_solve_small<T, L, E, false>;
+        auto pass = k_solve_pass<T, L, E, false>;
+        if (Row<T, L, E, true>::fits(A.s, A.ld, A.m)) {
+            small = k_solve_small<T, L, E, true>;
+            pass = k_solve_pass<T, L, E, true>;
+        }
+        if (A.n <= kSolveThreads / L * (kSmallScores / E)) {
+            A.iters = n_iters;
+            hipLaunchKernelGGL(small, dim3(1), dim3(kSolveThreads), 0, s, A);
+            if (hipGetLastError() != hipSuccess) st = SK_ERR_HIP;
+            return;
+        }
+        for (int k = 0; k < n_iters && st == SK_OK; ++k) {
+            A.last = k + 1 == n_iters;
+            hipLaunchKernelGGL(pass, dim3(A.groups), dim3(kSolveThreads), 0, s, A);
+            if (hipGetLastError() != hipSuccess) st = SK_ERR_HIP;
+            hipLaunchKernelGGL((k_solve_update<T>), dim3((unsigned)((A.m + 7) / 8)), dim3(kBlock), 0, s, A);
+            if (hipGetLastError() != hipSuccess) st = SK_ERR_HIP;
+            A.g_in = A.g;
+        }
+    });
+    return st;
 }
 
 size_t solve_ws_bytes(int64_t n, int64_t m) {
