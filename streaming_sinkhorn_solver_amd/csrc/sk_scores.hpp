@@ -52,7 +52,7 @@ inline int elem_size(int32_t dtype) { return dtype == SK_F32 ? 4 : 2; }
 __device__ __forceinline__ float s_ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float s_lg2(float x) { return __builtin_amdgcn_logf(x); }
 
-// ----- reductions over groups of L consecutive lanes (L = 4, 8, 16 or 64), result in every lane --------
+// ----- reductions over groups of L consecutive lanes (L = 4, 8, 16, 32 or 64), result in every lane --------
 // Inside a row of 16 lanes by quad permutations, half-row mirror and rotation;
 // across the four rows of a wave by the row swaps.
 template <int CTRL>
@@ -67,15 +67,17 @@ constexpr int kRor8 = 0x128;        // row_ror:8
 
 template <int L, class Op>
 __device__ __forceinline__ uint32_t lanes_reduce(uint32_t x, Op op) {
-    static_assert(L == 4 || L == 8 || L == 16 || L == 64, "lanes per row");
+    static_assert(L == 4 || L == 8 || L == 16 || L == 32 || L == 64, "lanes per row");
     x = op(x, dpp<kQuadXor1>(x));
     x = op(x, dpp<kQuadXor2>(x));
     if constexpr (L >= 8) x = op(x, dpp<kHalfMirror>(x));
     if constexpr (L >= 16) x = op(x, dpp<kRor8>(x));
-    if constexpr (L == 64) {
+    if constexpr (L >= 32) {
         auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
         x = op((uint32_t)r[0], (uint32_t)r[1]);
-        r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    }
+    if constexpr (L == 64) {
+        auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
         x = op((uint32_t)r[0], (uint32_t)r[1]);
     }
     return x;
@@ -93,6 +95,12 @@ struct OpAddF {
 };
 struct OpMaxU {
     __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
+};
+struct OpOr {
+    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a | b; }
+};
+struct OpAddU {
+    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a + b; }
 };
 struct OpMinU {
     __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; }
@@ -131,6 +139,10 @@ __device__ __forceinline__ double lanes_sum(double x) {
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
     return lanes_reduce<L>(x, OpMaxU());
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_sum_u(uint32_t x) {
+    return lanes_reduce<L>(x, OpAddU());
 }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_min(uint32_t x) {
@@ -201,6 +213,16 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 }
 __device__ __forceinline__ double unordered(uint64_t k) {
     return __builtin_bit_cast(double, k ^ ((k >> 63) ? 0x8000000000000000ull : 0xffffffffffffffffull));
+}
+
+// The k-th largest of the 64 lanes' keys (the same in every lane).
+__device__ __forceinline__ uint32_t kth_of_wave(uint32_t key, int k) {
+    uint32_t t = 0;
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t x = t | (1u << b);
+        if (__popcll(__ballot(key >= x)) >= k) t = x;
+    }
+    return t;
 }
 
 // ----- host-side checks ---------------------------------------------------------------

@@ -77,16 +77,6 @@ __device__ __forceinline__ void finish_top(const LpArgs& A, int64_t i, int r, ui
     A.top_logp[i * A.top + r] = S == 0.0f ? -INFINITY : (s - M) / A.eps - logf(S);
 }
 
-// The k-th largest of the 64 lanes' keys (the same in every lane).
-__device__ __forceinline__ uint32_t kth_of_wave(uint32_t key, int k) {
-    uint32_t t = 0;
-    for (int b = 31; b >= 0; --b) {
-        const uint32_t x = t | (1u << b);
-        if (__popcll(__ballot(key >= x)) >= k) t = x;
-    }
-    return t;
-}
-
 template <class T>
 struct Vec {
     static constexpr int n = 16 / sizeof(typename T::type);

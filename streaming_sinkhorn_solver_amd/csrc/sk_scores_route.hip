@@ -7,15 +7,19 @@
 // the sum of its group_top largest v); ties go to the lowest index.  The
 // weights come from act at the chosen experts, without the bias.
 //
-// One row per L lanes with E scores each (column e L + l), in registers; k
-// rounds of an argmax over ordered 32-bit keys, each a scan of the lane's keys
-// and four or six cross-lane steps.  The rounds are what the kernel spends
-// its time on, not the n m scores it reads.
+// One row per L lanes with E scores each, in registers.  Wide rows find the
+// (k + 1)-th largest of the lanes' maxima, a lower bound of the (k + 1)-th
+// largest value, and rank the few entries above it by counting; narrow rows, and
+// rows whose largest entries crowd into a few lanes, take k + 1 rounds of an argmax.
 //
 // The order of two values that are closer than the float32 rounding of act or
-// of the sum with the bias would depend on that rounding.  Rows where a pair
-// that decides the result is that close are chosen again with everything in
-// float64, so the result is that of the definition.
+// of the sum with the bias would depend on that rounding.  The choice is
+// therefore checked against error bounds, which is what the (k + 1)-th is for, and
+// rows where a pair that decides is too close are marked (their first index is
+// stored as its complement); a second kernel, which also counts the rows per
+// expert, chooses those again in float64, a workgroup each: the result is that of the
+// definition.  (With the float64 code in the first kernel its registers leave two
+// waves per SIMD, or spill, and one doubtful row holds up the end of the launch.)
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -27,6 +31,8 @@ constexpr int kRouteMaxCols = 1024;
 constexpr int kRouteMaxTop = 64;
 constexpr int kRouteMaxGroups = 64;
 constexpr int kRouteGroupsOfGrid = 2048;  // workgroups: eight per CU
+constexpr int kFinishRows = 128;          // rows that a workgroup of the second kernel takes at a time
+constexpr int kFinishGroups = 128;        // its workgroups, each of which adds up to m counts to memory
 
 struct RouteArgs {
     const void* s;
@@ -35,6 +41,7 @@ struct RouteArgs {
     int sigmoid;       // act: 0 softmax, 1 sigmoid
     const float* bias; // null: none
     int raw;           // v from the raw score (also where act alone decides: act keeps the scores' order)
+    int by_score;      // act without a bias: v for the groups' scores, the scores themselves inside them
     int n_group, topk_group, group_top, group_size;
     uint32_t group_magic;  // ceil(2^20 / group_size): (j * magic) >> 20 = j / group_size for j < 1024
     int k, renorm;
@@ -42,271 +49,445 @@ struct RouteArgs {
     int32_t* idx;
     float* weights;
     int32_t* counts;   // null: not wanted
-    int fill;          // counts were cleared before: add to them (else store)
+    int doubt;         // values are rounded: a row may be marked
+    int count_here;    // one workgroup and no doubt: the routing kernel counts
 };
 
-__device__ __forceinline__ float sigmoid_of(float x) { return 1.0f / (1.0f + s_ex2(-kLog2e * x)); }
-__device__ __forceinline__ double sigmoid_of(double x) { return 1.0 / (1.0 + exp(-x)); }
+__device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ __forceinline__ float exp_of(float x) { return s_ex2(kLog2e * x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
-// log sigmoid(x), accurate where sigmoid itself leaves the float32 range
-__device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.0f) - log1pf(exp_of(-fabsf(x))); }
-
-template <class R>
-struct KeyOf;
-template <>
-struct KeyOf<float> {
-    using type = uint32_t;
-};
-template <>
-struct KeyOf<double> {
-    using type = uint64_t;
-};
-
-template <int L>
-__device__ __forceinline__ uint32_t key_max(uint32_t k) {
-    return lanes_max<L>(k);
-}
-template <int L>
-__device__ __forceinline__ uint64_t key_max(uint64_t k) {
-    const uint32_t hi = lanes_max<L>((uint32_t)(k >> 32));
-    const uint32_t lo = lanes_max<L>((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
-    return (uint64_t)hi << 32 | lo;
+__device__ __forceinline__ float sigmoid_of(float x) { return rcp(1.0f + exp_of(-x)); }
+__device__ __forceinline__ double sigmoid_of(double x) { return 1.0 / (1.0 + exp(-x)); }
+// act exp(-shift) with shift >= the largest exponent of the row's choice, so that it does not underflow
+// together: exp(x - shift), or exp(min(x, 0) - shift) / (1 + exp(-|x|)).
+__device__ __forceinline__ float act_exponent(bool sigmoid, float x) { return sigmoid ? fminf(x, 0.0f) : x; }
+__device__ __forceinline__ float act_shifted(bool sigmoid, float x, float shift) {
+    const float e = exp_of(act_exponent(sigmoid, x) - shift);
+    return sigmoid ? e * rcp(1.0f + exp_of(-fabsf(x))) : e;
 }
 
-// The value that decides the choice, from the row's maximum M and sum S of
-// exponentials.  The same expression in float32 and float64.
+// The value that decides the choice, from the row's maximum M and the reciprocal of the
+// sum of its exponentials.  The same expression in float32 and float64.
 template <class R>
-__device__ __forceinline__ R choice_value(const RouteArgs& A, float s, float bias, float M, R S) {
+__device__ __forceinline__ R choice_value(const RouteArgs& A, float s, float bias, float M, R inv_S) {
     R v = (R)s;
-    if (!A.raw) v = A.sigmoid ? sigmoid_of((R)s) : exp_of((R)s - (R)M) / S;
+    if (!A.raw) v = A.sigmoid ? sigmoid_of((R)s) : exp_of((R)s - (R)M) * inv_S;
     return A.bias ? v + (R)bias : v;
 }
 
-// How far the float32 choice_value may be off, in steps of 2^-23.  The
-// exponential's argument d log2e carries three half-step roundings of |d| at
-// most, relative to act in the result; the exponentials, the sum of at most
-// 16 + 6 terms in turn, and the division add less than 30 half steps of act; the
-// sum with the bias adds half a step of v.
-__device__ __forceinline__ float choice_error(const RouteArgs& A, float s, float v, float M, float S) {
-    const float step = 0x1p-23f;
-    float err = A.bias ? fabsf(v) * step : 0.0f;
-    if (!A.raw) {
-        const float d = A.sigmoid ? fabsf(s) : M - s;
-        const float act = A.sigmoid ? sigmoid_of(s) : exp_of(s - M) / S;
-        err += act * (2.0f * d + 32.0f) * step;
-    }
+// How far the float32 choice_value may be off.  One step is 2^-23.
+//  softmax: an exponent d carries less than 1.25 d steps, the hardware's exp2 one;
+//    the sum of at most 16 + 6 additions 11 steps and its terms' own mean error, at most
+//    1.25 log m + 1 < 10; reciprocal and product 2: less than act (2 d + 32) steps.
+//  sigmoid: the exponential's error (1.25 |s| + 1) enters by 1 - sigmoid, and
+//    |s| sigmoid (1 - sigmoid) < 0.28; sum and reciprocal add 1.5: less than 4 steps.
+//  the sum with the bias adds half a step of the value.
+constexpr float kStep = 0x1p-23f;
+__device__ __forceinline__ float choice_error(const RouteArgs& A, float s, float v, float M, float inv_S) {
+    float err = A.bias ? fabsf(v) * kStep : 0.0f;
+    if (!A.raw) err += A.sigmoid ? 4.0f * kStep * fminf(1.0f, 2.0f * exp_of(s)) : exp_of(s - M) * inv_S * (2.0f * (M - s) + 32.0f) * kStep;
     return err;
 }
-
-struct RouteLds {
-    uint16_t* won;    // [kRouteMaxTop + 1] this row's choice, in order
-    void* tile;       // [m] keys of the row (groups only)
-    // of the n_group groups: keys of their scores, the scores and their float32 errors by rank, chosen or not
-    uint64_t* gkey;
-    float *gscore, *gerr;
-    uint8_t* gsel;
-};
-
-// Chooses the row's k experts (and, where one is left, the next after them)
-// into lds.won.  Returns the number of entries written; sets close when two
-// groups that decide were within their float32 error.
-template <class R, int L, int E>
-__device__ __forceinline__ int choose(const RouteArgs& A, const float (&s)[E], const float (&bias)[E], int l, float M,
-                                      R S, const RouteLds& lds, bool* close) {
-    using K = typename KeyOf<R>::type;
-    K key[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int j = e * L + l;
-        key[e] = j < A.m ? ordered(choice_value<R>(A, s[e], bias[e], M, S)) : (K)0;
-    }
-    int left = A.m;
-    if (A.n_group > 1) {
-        K* tile = static_cast<K*>(lds.tile);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (e * L + l < A.m) tile[e * L + l] = key[e];
-        wave_sync();
-        float err[kRouteMaxGroups / L];
-#pragma unroll
-        for (int gl = 0; gl < kRouteMaxGroups / L; ++gl) {
-            const int g = gl * L + l;
-            if (g >= A.n_group) break;
-            K k1 = 0, k2 = 0;
-            for (int q = 0; q < A.group_size; ++q) {
-                const K x = tile[g * A.group_size + q];
-                k2 = x > k1 ? k1 : (x > k2 ? x : k2);
-                k1 = x > k1 ? x : k1;
-            }
-            const R v1 = unordered(k1), v2 = A.group_top == 2 ? unordered(k2) : (R)0;
-            lds.gkey[g] = (uint64_t)ordered(v1 + v2);
-            // choice_error of both values and the sum's rounding.  act (2 d + 32) is at most 33 where a bias
-            // hides act, and at most 2^8 v where it does not (d <= 104, or act is zero)
-            const float size = fabsf((float)v1) + fabsf((float)v2);
-            err[gl] = size * 0x1p-22f + (A.raw ? 0.0f : A.bias ? 0x1p-16f : size * 0x1p-15f);
-        }
-        wave_sync();
-#pragma unroll
-        for (int gl = 0; gl < kRouteMaxGroups / L; ++gl) {
-            const int g = gl * L + l;
-            if (g >= A.n_group) break;
-            const uint64_t mine = lds.gkey[g];
-            int rank = 0;
-            for (int q = 0; q < A.n_group; ++q) {
-                const uint64_t x = lds.gkey[q];
-                rank += x > mine || (x == mine && q < g) ? 1 : 0;
-            }
-            lds.gsel[g] = rank < A.topk_group;
-            lds.gscore[rank] = (float)unordered((K)mine);
-            lds.gerr[rank] = err[gl];
-        }
-        wave_sync();
-        if (A.topk_group < A.n_group) {
-            const float in = lds.gscore[A.topk_group - 1], out = lds.gscore[A.topk_group];
-            const float tol = lds.gerr[A.topk_group - 1] + lds.gerr[A.topk_group];
-            if (in - out <= tol && (A.bias || !A.raw || A.group_top == 2)) *close = true;
-        }
-        left = A.topk_group * A.group_size;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t j = e * L + l;
-            if ((int)j < A.m && !lds.gsel[(j * A.group_magic) >> 20]) key[e] = 0;
-        }
-    }
-    const int rounds = left > A.k ? A.k + 1 : A.k;
-    for (int r = 0; r < rounds; ++r) {
-        K best = key[0];
-#pragma unroll
-        for (int e = 1; e < E; ++e) best = key[e] > best ? key[e] : best;
-        best = key_max<L>(best);
-        uint32_t at = 0xffffffffu;
-#pragma unroll
-        for (int e = E - 1; e >= 0; --e) at = key[e] == best ? (uint32_t)(e * L + l) : at;
-        at = lanes_min<L>(at);
-#pragma unroll
-        for (int e = 0; e < E; ++e) key[e] = (uint32_t)(e * L + l) == at ? (K)0 : key[e];
-        if (l == 0) lds.won[r] = (uint16_t)at;
-    }
-    wave_sync();
-    return rounds;
+// The most that act's part of it can be in the row (act (2 d + 32) falls with d).
+__device__ __forceinline__ float act_error(const RouteArgs& A, float inv_S) {
+    return A.raw ? 0.0f : A.sigmoid ? 4.0f * kStep : 32.0f * kStep * inv_S;
 }
 
-template <class T, int L, int E>
-__global__ __launch_bounds__(kBlock) void k_route(RouteArgs A) {
-    constexpr int kSlots = kBlock / L;
-    extern __shared__ uint64_t dyn[];
-    __shared__ uint16_t won[kSlots][kRouteMaxTop + 2];
-    const int l = threadIdx.x % L, slot = threadIdx.x / L;
-    // dynamic: counts [m], then, with groups, per row slot the keys [m] and the groups' keys, scores and flags
-    int32_t* hist = reinterpret_cast<int32_t*>(dyn);
-    char* p = reinterpret_cast<char*>(dyn) + (A.counts ? ((size_t)A.m * 4 + 7) / 8 * 8 : 0);
-    RouteLds lds{won[slot], nullptr, nullptr, nullptr, nullptr, nullptr};
-    if (A.n_group > 1) {
-        const size_t row = (size_t)A.m * 8 + (size_t)A.n_group * 24;
-        char* q = p + (size_t)slot * row;
-        lds.tile = q;
-        lds.gkey = reinterpret_cast<uint64_t*>(q + (size_t)A.m * 8);
-        lds.gscore = reinterpret_cast<float*>(lds.gkey + A.n_group);
-        lds.gerr = lds.gscore + A.n_group;
-        lds.gsel = reinterpret_cast<uint8_t*>(lds.gerr + A.n_group);
+// The float32 keys of the routing kernel are the values themselves: a NaN value
+// has been made -inf, and a column that takes no part is a NaN, which the
+// hardware's maximum and every comparison pass over.
+__device__ __forceinline__ float key_of(float v) { return fmaxf(v, -INFINITY); }
+
+// LDS of one wave (64 / L rows): the rows' scores (their keys while groups are chosen), and small arrays.
+template <int L, int E>
+struct alignas(16) RouteWave {
+    static constexpr int kRows = 64 / L, kList = 2 * L;
+    float s[kRows][L * E];
+    union {  // at different times: candidates, lanes' maxima, the groups' scores
+        uint64_t list[kRows][kList];
+        float lane_key[kRows][L];
+        float gscore[kRows][kRouteMaxGroups];
+    };
+    int count[kRows];
+    uint16_t won[kRows][kRouteMaxTop + 1];
+};
+
+// The kk-th largest of the row's lanes' keys (NaN for a lane without one), kk at most the lanes that have one;
+// -inf if there are fewer.  Counted through LDS.
+template <int L, int E>
+__device__ __forceinline__ float kth_of_lanes(RouteWave<L, E>& W, float key, int l, int row, int kk) {
+    W.lane_key[row][l] = key;
+    wave_sync();
+    int rank = 0;
+#pragma unroll
+    for (int q = 0; q < L; q += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&W.lane_key[row][q]);
+        rank += (x.x > key ? 1 : 0) + (x.y > key ? 1 : 0) + (x.z > key ? 1 : 0) + (x.w > key ? 1 : 0);
     }
-    if (A.counts) {
-        for (int j = threadIdx.x; j < A.m; j += kBlock) hist[j] = 0;
-        __syncthreads();
+    wave_sync();
+    // the ranks below kk belong to the kk largest and what equals the last of them
+    const float low = -lanes_max<L>(rank < kk ? -key : -INFINITY);
+    const uint32_t some = lanes_sum_u<L>(key == key && rank < kk ? 1u : 0u);
+    return some >= (uint32_t)kk ? low : -INFINITY;
+}
+
+// Sets to NaN the keys of columns outside the row's best groups.  close: whether the
+// last group taken and the first left out are within their errors.
+template <class Rw, int L, int E>
+__device__ __forceinline__ void keep_groups(const RouteArgs& A, RouteWave<L, E>& W, float (&key)[E], int l, int row,
+                                            float act_err, float inv_S, bool* close) {
+    // the lanes of a row share its groups out, `per` lanes to a group (a power of two)
+    int per = 1;
+    while (2 * per * A.n_group <= L) per *= 2;
+    const int share = (A.group_size + per - 1) / per;  // columns of one lane
+    uint64_t taken = 0;                                // bit g: group g is one of the best
+    float worst_err = 0.0f;
+    for (int g0 = 0; g0 < A.n_group; g0 += L / per) {
+        const int g = g0 + l / per, sub = l % per;
+        float k1 = -INFINITY, k2 = -INFINITY;
+        if (g < A.n_group) {
+            // each lane starts somewhere else in its group, so the lanes do not meet in one bank
+            int q = l % share;
+            for (int n = 0; n < share; ++n) {
+                const int at = sub * share + q;
+                const float x = at < A.group_size ? W.s[row][g * A.group_size + at] : -INFINITY;
+                k2 = fmaxf(k2, fminf(k1, x));
+                k1 = fmaxf(k1, x);
+                if (++q == share) q = 0;
+            }
+        }
+        for (int o = 1; o < per; o *= 2) {
+            const float y1 = __shfl_xor(k1, o), y2 = __shfl_xor(k2, o);
+            k2 = fmaxf(fminf(k1, y1), fmaxf(k2, y2));
+            k1 = fmaxf(k1, y1);
+        }
+        const float v1 = k1, v2 = A.group_top == 2 ? k2 : 0.0f;
+        const float sum = key_of(v1 + v2);
+        float err = fabsf(sum) * kStep;
+        if (A.bias) err += (fabsf(v1) + fabsf(v2)) * kStep + 2.0f * act_err;
+        // without a bias v is act itself: 4 steps of it, or 2 d + 32 with d = log(1 / (act S))
+        if (!A.bias && !A.raw)
+            err += (v1 + v2) * kStep * (A.sigmoid ? 4.0f : 32.0f + 2.0f * kLn2 * fmaxf(0.0f, s_lg2(inv_S) - s_lg2(fmaxf(v2, 0x1p-126f))));
+        if (g < A.n_group) {
+            if (sum > -INFINITY) worst_err = fmaxf(worst_err, err);  // (a masked group's score is exact)
+            if (sub == 0) W.gscore[row][g] = sum;
+        }
     }
-    float bias[E];
+    worst_err = lanes_max<L>(worst_err);
+    wave_sync();
+    float in = INFINITY, out = -INFINITY;  // the last score taken, the first left out
+    for (int g = l; g < A.n_group; g += L) {
+        const float mine = W.gscore[row][g];
+        int rank = 0;
+        for (int q = 0; q < A.n_group; ++q) {
+            const float x = W.gscore[row][q];
+            rank += x > mine || (x == mine && q < g) ? 1 : 0;
+        }
+        if (rank < A.topk_group) {
+            taken |= 1ull << g;
+            in = fminf(in, mine);
+        } else {
+            out = fmaxf(out, mine);
+        }
+    }
+    const uint32_t lo = lanes_reduce<L>((uint32_t)taken, OpOr()), hi = lanes_reduce<L>((uint32_t)(taken >> 32), OpOr());
+    in = -lanes_max<L>(-in);
+    out = lanes_max<L>(out);
+    if (A.doubt && A.topk_group < A.n_group && in - out <= 2.0f * worst_err) *close = true;
+    wave_sync();
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int j = e * L + l;
-        bias[e] = A.bias && j < A.m ? A.bias[j] : 0.0f;
+        const uint32_t j = Rw::col(e, l), g = (j * A.group_magic) >> 20;
+        const uint32_t bit = (g < 32 ? lo >> g : hi >> (g - 32)) & 1u;
+        key[e] = bit ? key[e] : NAN;
     }
-    for (int64_t i0 = (int64_t)blockIdx.x * kSlots; i0 < A.n; i0 += (int64_t)gridDim.x * kSlots) {
-        const int64_t i = i0 + slot;
-        const bool on = i < A.n;
-        const typename T::type* row = static_cast<const typename T::type*>(A.s) + (on ? i : i0) * A.ld;
-        float s[E];
+}
+
+// The rows' first `rounds` columns in descending order of their keys, ties by the lower column, into W.won.
+template <class Rw, int L, int E, class Key>
+__device__ __forceinline__ void choose(RouteWave<L, E>& W, float (&key)[E], int l, int row, int rounds, Key key_at) {
+    if constexpr (L >= 16) {
+        // The bound is loose when nearly every lane's maximum is wanted, and for two rounds a plain argmax is as short.
+        if (rounds > 2 && rounds <= L - L / 4) {
+            float best = key[0];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int j = e * L + l;
-            s[e] = T::to(row[j < A.m ? j : A.m - 1]);
-            if (j >= A.m) s[e] = -INFINITY;
+            for (int e = 1; e < E; ++e) best = fmaxf(best, key[e]);
+            const float t = kth_of_lanes<L, E>(W, best, l, row, rounds);
+            if (l == 0) W.count[row] = 0;
+            W.list[row][l] = 0;
+            W.list[row][l + L] = 0;
+            uint32_t mask = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) mask |= key[e] >= t ? 1u << e : 0u;
+            wave_sync();
+            int at = mask ? atomicAdd(&W.count[row], __popc(mask)) : 0;
+            wave_sync();
+            const int have = W.count[row];
+            if (!__any(have > RouteWave<L, E>::kList)) {
+                while (mask) {
+                    const int j = Rw::col(__builtin_ctz(mask), l);
+                    mask &= mask - 1;
+                    W.list[row][at++] = (uint64_t)ordered(key_at(j)) << 32 | (uint32_t)~j;
+                }
+                wave_sync();
+                const uint64_t a = W.list[row][l], b = W.list[row][l + L];
+                int ra = 0, rb = 0;
+                const int most = (int)lanes_max<64>((uint32_t)have);
+                if (most <= L) {
+                    for (int c = 0; c < most; ++c) ra += W.list[row][c] > a ? 1 : 0;
+                } else {
+                    for (int c = 0; c < most; ++c) {
+                        const uint64_t x = W.list[row][c];
+                        ra += x > a ? 1 : 0;
+                        rb += x > b ? 1 : 0;
+                    }
+                }
+                if (a && ra < rounds) W.won[row][ra] = (uint16_t)~(uint32_t)a;
+                if (b && rb < rounds) W.won[row][rb] = (uint16_t)~(uint32_t)b;
+                wave_sync();
+                return;
+            }
         }
+    }
+    for (int r = 0; r < rounds; ++r) {
+        float best = key[0];
+#pragma unroll
+        for (int e = 1; e < E; ++e) best = fmaxf(best, key[e]);
+        best = lanes_max<L>(best);
+        uint32_t at = 0xffffffffu;
+#pragma unroll
+        for (int e = E - 1; e >= 0; --e) at = key[e] == best ? (uint32_t)Rw::col(e, l) : at;
+        at = lanes_min<L>(at);
+#pragma unroll
+        for (int e = 0; e < E; ++e) key[e] = (uint32_t)Rw::col(e, l) == at ? NAN : key[e];
+        if (l == 0) W.won[row][r] = (uint16_t)at;
+    }
+    wave_sync();
+}
+
+// Weights of the lane's entries r = l, l + L, ... of the row's choice `won`; score(j) is the row's score at j.
+template <int L, class Score>
+__device__ __forceinline__ void store_weights(const RouteArgs& A, const uint16_t* won, int l, int64_t i, bool on, float M,
+                                              float inv_S, Score score) {
+    float shift = 0.0f, inv = 1.0f;
+    if (A.renorm) {
+        shift = kNegBig;
+        for (int r = l; r < A.k; r += L) shift = fmaxf(shift, act_exponent(A.sigmoid, score(won[r])));
+        shift = lanes_max<L>(shift);
+        float sum = 0.0f;
+        for (int r = l; r < A.k; r += L) sum += act_shifted(A.sigmoid, score(won[r]), shift);
+        sum = lanes_sum<L>(sum);
+        inv = sum == 0.0f ? 1.0f : 1.0f / sum;  // every chosen score is masked: weights 0
+    }
+    if (!on) return;
+    for (int r = l; r < A.k; r += L) {
+        const float x = score(won[r]);
+        const float q = A.renorm ? act_shifted(A.sigmoid, x, shift) * inv : A.sigmoid ? sigmoid_of(x) : exp_of(x - M) * inv_S;
+        A.weights[i * A.k + r] = A.scale * q;
+    }
+}
+
+template <class T, int L, int E, bool V>
+__global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
+    constexpr int kSlots = kBlock / L;
+    using Rw = Row<T, L, E, V>;
+    using Elem = typename T::type;
+    __shared__ RouteWave<L, E> waves[kBlock / 64];
+    __shared__ int32_t hist[L * E];
+    __shared__ float bias[L * E];
+    const int lane = threadIdx.x & 63, l = threadIdx.x % L, row = lane / L;
+    RouteWave<L, E>& W = waves[threadIdx.x / 64];
+    if (A.counts) {
+        for (int j = threadIdx.x; j < A.m; j += kBlock) {
+            if (A.count_here)
+                hist[j] = 0;
+            else if (blockIdx.x == 0)
+                A.counts[j] = 0;  // cleared here for the kernel that counts
+        }
+    }
+    for (int j = threadIdx.x; j < L * E; j += kBlock) bias[j] = A.bias && j < A.m ? A.bias[j] : 0.0f;
+    __syncthreads();
+    const int left = A.n_group > 1 ? A.topk_group * A.group_size : A.m;
+    const int rounds = left > A.k ? A.k + 1 : A.k;
+    for (int64_t i0 = (int64_t)blockIdx.x * kSlots; i0 < A.n; i0 += (int64_t)gridDim.x * kSlots) {
+        const int64_t i = i0 + threadIdx.x / L;
+        const bool on = i < A.n;
+        float s[E];
+        Rw::load(static_cast<const Elem*>(A.s) + (on ? i : i0) * A.ld, l, A.m, s);
         // softmax statistics; an empty row keeps S = 0
-        float M = kNegBig, S = 0.0f;
-        if (!A.sigmoid) {
+        float M = kNegBig, inv_S = 1.0f;
+        if (!A.sigmoid && (!A.raw || !A.renorm)) {
+            float S = 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) M = fmaxf(M, s[e]);
             M = lanes_max<L>(M);
 #pragma unroll
             for (int e = 0; e < E; ++e) S += exp_of(s[e] - M);
             S = lanes_sum<L>(S);
+            inv_S = S == 0.0f ? 1.0f : 1.0f / S;  // act = 0 in an empty row
         }
-        const float S1 = S == 0.0f ? 1.0f : S;  // act = 0 in an empty row
-        bool close = false;
-        int rounds = choose<float, L, E>(A, s, bias, l, M, S1, lds, &close);
-        if (A.bias || !A.raw) {  // values that were rounded: neighbours in the order must be apart
-            for (int r = l; r + 1 < rounds; r += L) {
-                const int j0 = lds.won[r], j1 = lds.won[r + 1];
-                const float s0 = T::to(row[j0]), s1 = T::to(row[j1]);
-                const float v0 = choice_value<float>(A, s0, A.bias ? A.bias[j0] : 0.0f, M, S1);
-                const float v1 = choice_value<float>(A, s1, A.bias ? A.bias[j1] : 0.0f, M, S1);
-                const float tol = choice_error(A, s0, v0, M, S1) + choice_error(A, s1, v1, M, S1);
-                if (v0 - v1 <= tol) close = true;
-            }
-        }
-        if (__any(close)) {
-            double S2 = 0.0;
-            if (!A.sigmoid) {
+        auto key_at = [&](int j) {
+            return key_of(A.by_score ? W.s[row][j] : choice_value<float>(A, W.s[row][j], bias[j], M, inv_S));
+        };
+        float key[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) S2 += exp((double)s[e] - (double)M);
-                S2 = lanes_sum<L>(S2);
-                if (S2 == 0.0) S2 = 1.0;
-            }
+        for (int e = 0; e < E; ++e) {
+            const int j = Rw::col(e, l);
+            key[e] = j < A.m ? key_of(choice_value<float>(A, s[e], bias[j], M, inv_S)) : NAN;
+        }
+        bool close = false;
+        const float act_err = act_error(A, inv_S);
+        if (A.n_group > 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) W.s[row][Rw::col(e, l)] = key[e];
             wave_sync();
-            bool ignored = false;
-            choose<double, L, E>(A, s, bias, l, M, S2, lds, &ignored);
-        }
-        // weights of the chosen: q = act, or act over its sum taken relative to the largest
-        float top = kNegBig, sum = 0.0f;
-        if (A.renorm) {
-            for (int r = l; r < A.k; r += L) {
-                const float x = T::to(row[lds.won[r]]);
-                top = fmaxf(top, A.sigmoid ? log_sigmoid(x) : x);
-            }
-            top = lanes_max<L>(top);
-            for (int r = l; r < A.k; r += L) {
-                const float x = T::to(row[lds.won[r]]);
-                sum += exp_of((A.sigmoid ? log_sigmoid(x) : x) - top);
-            }
-            sum = lanes_sum<L>(sum);
-            if (sum == 0.0f) sum = 1.0f;  // every chosen score is masked: weights 0
-        }
-        if (on) {
-            for (int r = l; r < A.k; r += L) {
-                const int j = lds.won[r];
-                const float x = T::to(row[j]);
-                float q;
-                if (A.renorm)
-                    q = exp_of((A.sigmoid ? log_sigmoid(x) : x) - top) / sum;
-                else
-                    q = A.sigmoid ? sigmoid_of(x) : exp_of(x - M) / S1;
-                A.idx[i * A.k + r] = j;
-                A.weights[i * A.k + r] = A.scale * q;
-                if (A.counts) atomicAdd(&hist[j], 1);
+            keep_groups<Rw, L, E>(A, W, key, l, row, act_err, inv_S, &close);
+            if (A.by_score) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) key[e] = key[e] == key[e] ? key_of(s[e]) : NAN;
             }
         }
+#pragma unroll
+        for (int e = 0; e < E; ++e) W.s[row][Rw::col(e, l)] = s[e];
+        wave_sync();
+        choose<Rw, L, E>(W, key, l, row, rounds, key_at);
+        if (A.doubt && A.bias) {  // neighbours in the order must be apart
+            for (int r = l; r + 1 < rounds; r += L) {
+                const int j0 = W.won[row][r], j1 = W.won[row][r + 1];
+                const float v0 = key_at(j0), v1 = key_at(j1);
+                // the first column left out stands for all others, whose act may be larger
+                const float e1 = r + 1 == A.k ? fabsf(v1) * kStep + act_err : choice_error(A, W.s[row][j1], v1, M, inv_S);
+                if (v0 - v1 <= choice_error(A, W.s[row][j0], v0, M, inv_S) + e1) close = true;
+            }
+        }
+        const bool marked = lanes_max<L>(close ? 1u : 0u) != 0;
+        for (int r = l; on && r < A.k; r += L) {
+            const int j = W.won[row][r];
+            A.idx[i * A.k + r] = marked && r == 0 ? ~j : j;
+            if (A.count_here) atomicAdd(&hist[j], 1);
+        }
+        store_weights<L>(A, W.won[row], l, i, on, M, inv_S, [&](int j) { return W.s[row][j]; });
         wave_sync();
     }
-    if (A.counts) {
+    if (A.count_here) {
         __syncthreads();
-        for (int j = threadIdx.x; j < A.m; j += kBlock) {
-            if (!A.fill)
-                A.counts[j] = hist[j];
-            else if (hist[j])
-                atomicAdd(&A.counts[j], hist[j]);  // whole numbers: the order does not matter
-        }
+        for (int j = threadIdx.x; j < A.m; j += kBlock) A.counts[j] = hist[j];
     }
+}
+
+// After k_route: chooses the marked rows in float64 and counts the rows per expert into cleared counts (whole numbers,
+// so the order does not matter).  A workgroup takes kFinishRows rows at a time.
+template <class T>
+__global__ __launch_bounds__(kBlock) void k_route_finish(RouteArgs A) {
+    constexpr int kWaves = kBlock / 64;
+    __shared__ unsigned long long key[kRouteMaxCols], first[kRouteMaxGroups], second[kRouteMaxGroups];
+    __shared__ int owner[kRouteMaxGroups];
+    __shared__ double red[kWaves];
+    __shared__ uint32_t lane_top[kWaves][64];
+    __shared__ uint16_t list[kRouteMaxCols];
+    __shared__ int have;
+    __shared__ uint16_t won[kRouteMaxTop];
+    __shared__ int32_t hist[kRouteMaxCols];
+    __shared__ uint8_t todo[kFinishRows];
+    __shared__ int many;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+    // One row by the whole workgroup: values, ranks by counting, weights.
+    auto exact = [&](int64_t i) {
+        const typename T::type* s = static_cast<const typename T::type*>(A.s) + i * A.ld;
+        float M = kNegBig, S1 = 1.0f;
+        double inv_S = 1.0;
+        if (!A.sigmoid) {
+            for (int j = lane; j < A.m; j += 64) M = fmaxf(M, T::to(s[j]));
+            M = lanes_max<64>(M);
+            double S = 0.0;
+            for (int j = tid; j < A.m; j += kBlock) S += exp((double)T::to(s[j]) - (double)M);
+            S = lanes_sum<64>(S);
+            if (lane == 0) red[wave] = S;
+            __syncthreads();
+            S = 0.0;
+            for (int w = 0; w < kWaves; ++w) S += red[w];
+            if (S != 0.0) inv_S = 1.0 / S, S1 = (float)S;
+        }
+        for (int j = tid; j < A.m; j += kBlock)
+            key[j] = ordered(choice_value<double>(A, T::to(s[j]), A.bias ? A.bias[j] : 0.0f, M, inv_S));
+        __syncthreads();
+        if (A.n_group > 1) {
+            // the groups' two largest keys; of equal largest ones the lowest column is the first
+            for (int g = tid; g < A.n_group; g += kBlock) first[g] = second[g] = 0, owner[g] = INT_MAX;
+            __syncthreads();
+            for (int j = tid; j < A.m; j += kBlock) atomicMax(&first[j / A.group_size], key[j]);
+            __syncthreads();
+            if (A.group_top == 2) {
+                for (int j = tid; j < A.m; j += kBlock)
+                    if (key[j] == first[j / A.group_size]) atomicMin(&owner[j / A.group_size], j);
+                __syncthreads();
+                for (int j = tid; j < A.m; j += kBlock)
+                    if (owner[j / A.group_size] != j) atomicMax(&second[j / A.group_size], key[j]);
+                __syncthreads();
+                for (int g = tid; g < A.n_group; g += kBlock) first[g] = ordered(unordered((uint64_t)first[g]) + unordered((uint64_t)second[g]));
+                __syncthreads();
+            }
+            for (int j = tid; j < A.m; j += kBlock) {
+                const int g = j / A.group_size;
+                int rank = 0;
+                for (int q = 0; q < A.n_group; ++q) rank += first[q] > first[g] || (first[q] == first[g] && q < g) ? 1 : 0;
+                if (rank >= A.topk_group)
+                    key[j] = 0;
+                else if (A.by_score)
+                    key[j] = ordered((double)T::to(s[j]));
+            }
+        }
+        // the k-th largest of 64 classes' maxima (upper halves of the keys) bounds the k-th largest key from below
+        uint32_t top = 0;
+        for (int j = tid; j < A.m; j += kBlock) top = max(top, (uint32_t)(key[j] >> 32));
+        lane_top[wave][lane] = top;
+        if (tid == 0) have = 0;
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w) top = max(top, lane_top[w][lane]);
+        top = max(kth_of_wave(top, A.k), 1u);
+        for (int j = tid; j < A.m; j += kBlock)
+            if ((uint32_t)(key[j] >> 32) >= top) list[atomicAdd(&have, 1)] = (uint16_t)j;
+        __syncthreads();
+        const int count = have;
+        for (int c = tid; c < count; c += kBlock) {
+            const int j = list[c];
+            const uint64_t mine = key[j];
+            int rank = 0;
+            for (int q = 0; q < count; ++q) {
+                const int jq = list[q];
+                const uint64_t x = key[jq];
+                rank += x > mine || (x == mine && jq < j) ? 1 : 0;
+            }
+            if (rank < A.k) {
+                won[rank] = (uint16_t)j;
+                A.idx[i * A.k + rank] = j;
+            }
+        }
+        __syncthreads();
+        if (wave == 0) store_weights<64>(A, won, lane, i, true, M, 1.0f / S1, [&](int j) { return T::to(s[j]); });
+        __syncthreads();
+    };
+    if (A.counts)
+        for (int j = tid; j < A.m; j += kBlock) hist[j] = 0;
+    for (int64_t i0 = (int64_t)blockIdx.x * kFinishRows; i0 < A.n; i0 += (int64_t)gridDim.x * kFinishRows) {
+        if (A.doubt) {
+            if (tid == 0) many = 0;
+            __syncthreads();
+            const int64_t i = i0 + tid;
+            if (tid < kFinishRows && i < A.n && A.idx[i * A.k] < 0) todo[atomicAdd(&many, 1)] = (uint8_t)tid;
+            __syncthreads();
+            for (int q = 0; q < many; ++q) exact(i0 + todo[q]);
+        }
+        __syncthreads();
+        if (A.counts) {
+            const int64_t end = min((int64_t)A.n, i0 + kFinishRows) * A.k;
+            for (int64_t q = i0 * A.k + tid; q < end; q += kBlock) atomicAdd(&hist[A.idx[q]], 1);
+        }
+        __syncthreads();
+    }
+    if (A.counts)
+        for (int j = tid; j < A.m; j += kBlock)
+            if (hist[j]) atomicAdd(&A.counts[j], hist[j]);
 }
 
 struct RouteGradArgs {
@@ -358,14 +539,14 @@ __global__ __launch_bounds__(kBlock) void k_route_grad(RouteGradArgs A) {
                 const int j = idx[r];
                 if ((unsigned)j >= (unsigned)A.m) continue;
                 const float x = T::to(row[j]);
-                top = fmaxf(top, A.sigmoid ? log_sigmoid(x) : x);
+                top = fmaxf(top, act_exponent(A.sigmoid, x));
             }
             top = lanes_max<L>(top);
             for (int r = l; r < A.k; r += L) {
                 const int j = idx[r];
                 if ((unsigned)j >= (unsigned)A.m) continue;
                 const float x = T::to(row[j]);
-                sum += exp_of((A.sigmoid ? log_sigmoid(x) : x) - top);
+                sum += act_shifted(A.sigmoid, x, top);
             }
             sum = lanes_sum<L>(sum);
             if (sum == 0.0f) sum = 1.0f;
@@ -377,7 +558,7 @@ __global__ __launch_bounds__(kBlock) void k_route_grad(RouteGradArgs A) {
             float q = 0.0f;
             if (in) {
                 if (A.renorm)
-                    q = exp_of((A.sigmoid ? log_sigmoid(x) : x) - top) / sum;
+                    q = act_shifted(A.sigmoid, x, top) / sum;
                 else
                     q = A.sigmoid ? sigmoid_of(x) : exp_of(x - M) / S;
             }
@@ -407,7 +588,7 @@ __global__ __launch_bounds__(kBlock) void k_route_grad(RouteGradArgs A) {
             if (A.renorm) {
                 int copies = 0;
                 for (int u = 0; u < A.k; ++u) copies += place[slot][u] == j ? 1 : 0;
-                const float q = exp_of((A.sigmoid ? log_sigmoid(x) : x) - top) / sum;
+                const float q = act_shifted(A.sigmoid, x, top) / sum;
                 total -= (float)copies * q * inner;
             }
             if (A.sigmoid) total *= sigmoid_of(-x);
@@ -426,49 +607,54 @@ __global__ __launch_bounds__(kBlock) void k_route_grad(RouteGradArgs A) {
     }
 }
 
+// f(lanes per row, scores per lane) for rows of m scores: as few lanes as hold the row at 16 scores each or less.
 template <class F>
 void by_width(int m, F f) {
+    using std::integral_constant;
     if (m <= 8)
-        f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+        f(integral_constant<int, 4>(), integral_constant<int, 2>());
     else if (m <= 16)
-        f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+        f(integral_constant<int, 4>(), integral_constant<int, 4>());
     else if (m <= 32)
-        f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
+        f(integral_constant<int, 4>(), integral_constant<int, 8>());
     else if (m <= 64)
-        f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+        f(integral_constant<int, 8>(), integral_constant<int, 8>());
     else if (m <= 128)
-        f(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
+        f(integral_constant<int, 16>(), integral_constant<int, 8>());
     else if (m <= 256)
-        f(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
+        f(integral_constant<int, 16>(), integral_constant<int, 16>());
     else if (m <= 512)
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+        f(integral_constant<int, 64>(), integral_constant<int, 8>());
     else
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+        f(integral_constant<int, 64>(), integral_constant<int, 16>());
 }
 
-int route_slots(int m) { return m <= 8 ? kBlock / 8 : m <= 256 ? kBlock / 16 : kBlock / 64; }
-
-unsigned route_grid(int64_t n, int m) {
-    const int slots = route_slots(m);
+unsigned route_grid(int64_t n, int lanes) {
+    const int slots = kBlock / lanes;
     return (unsigned)std::min<int64_t>((n + slots - 1) / slots, kRouteGroupsOfGrid);
 }
 
 template <class T>
-hipError_t launch_route(const RouteArgs& A, hipStream_t s) {
-    size_t lds = A.counts ? ((size_t)A.m * 4 + 7) / 8 * 8 : 0;
-    if (A.n_group > 1) lds += (size_t)route_slots(A.m) * ((size_t)A.m * 8 + (size_t)A.n_group * 24);
-    by_width(A.m, [&](auto l, auto e) {
-        hipLaunchKernelGGL((k_route<T, decltype(l)::value, decltype(e)::value>), dim3(route_grid(A.n, A.m)),
-                           dim3(kBlock), lds, s, A);
+hipError_t launch_route(RouteArgs A, hipStream_t s) {
+    by_width(A.m, [&](auto lanes, auto per_lane) {
+        constexpr int L = decltype(lanes)::value, E = decltype(per_lane)::value;
+        const unsigned grid = route_grid(A.n, L);
+        A.count_here = A.counts && grid == 1 && !A.doubt;
+        auto kernel = Row<T, L, E, true>::fits(A.s, A.ld, A.m) ? k_route<T, L, E, true> : k_route<T, L, E, false>;
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(kBlock), 0, s, A);
     });
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !(A.doubt || (A.counts && !A.count_here))) return e;
+    const int64_t grid = std::min<int64_t>(((int64_t)A.n + kFinishRows - 1) / kFinishRows, kFinishGroups);
+    hipLaunchKernelGGL((k_route_finish<T>), dim3((unsigned)grid), dim3(kBlock), 0, s, A);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_route_grad(const RouteGradArgs& A, hipStream_t s) {
-    by_width(A.m, [&](auto l, auto e) {
-        hipLaunchKernelGGL((k_route_grad<T, decltype(l)::value, decltype(e)::value>), dim3(route_grid(A.n, A.m)),
-                           dim3(kBlock), 0, s, A);
+    by_width(A.m, [&](auto lanes, auto per_lane) {
+        constexpr int L = decltype(lanes)::value, E = decltype(per_lane)::value;
+        hipLaunchKernelGGL((k_route_grad<T, L, E>), dim3(route_grid(A.n, L)), dim3(kBlock), 0, s, A);
     });
     return hipGetLastError();
 }
@@ -515,18 +701,20 @@ int sk_scores_route(const void* scores, int32_t dtype, int64_t n, int64_t m, int
     A.group_magic = (uint32_t)(((1u << 20) + A.group_size - 1) / A.group_size);
     // act rises with the score: without a bias and without sums of it, the scores decide, exactly
     A.raw = select_on == 1 || (!bias && (n_group == 1 || group_top == 1));
+    A.by_score = !A.raw && !bias;
+    A.doubt = bias || !A.raw || (n_group > 1 && topk_group < n_group && group_top == 2);
     A.k = k;
     A.renorm = renorm;
     A.scale = scale;
     A.idx = idx;
     A.weights = weights;
     A.counts = counts;
-    A.fill = n == 0 || route_grid(n, A.m) > 1;
-    if (counts && A.fill) {
+    if (n == 0) {
+        if (!counts) return SK_OK;
         hipLaunchKernelGGL(k_clear_counts, dim3((unsigned)((m + kBlock - 1) / kBlock)), dim3(kBlock), 0, s, counts, (int)m);
         SK_TRY_LAUNCH(hipGetLastError());
+        return SK_OK;
     }
-    if (n == 0) return SK_OK;
     SK_TRY_LAUNCH(dtype == SK_F32    ? launch_route<F32>(A, s)
                   : dtype == SK_BF16 ? launch_route<Bf16>(A, s)
                                      : launch_route<F16>(A, s));
