@@ -184,7 +184,17 @@ struct Row {
         fetch(row, l, m, raw);
         get(raw, l, m, s);
     }
-    // Whether the rows of a matrix can be read in runs.
+    __device__ static void store(Elem* row, int l, int m, const float (&s)[E]) {
+#pragma unroll
+        for (int q = 0; q < E / W; ++q) {
+            const int j = col(q * W, l);
+            Run r;
+#pragma unroll
+            for (int e = 0; e < W; ++e) r.v[e] = T::from(s[q * W + e]);
+            if (j < m) *reinterpret_cast<Run*>(row + j) = r;
+        }
+    }
+    // Whether the rows of a matrix can be read and written in runs.
     static bool fits(const void* p, int64_t ld, int64_t m) {
         return W > 1 && m % W == 0 && ld % W == 0 && reinterpret_cast<uintptr_t>(p) % (W * sizeof(Elem)) == 0;
     }

@@ -504,104 +504,98 @@ struct RouteGradArgs {
 //   softmax: ds_j = p_j (dq_j - inner); renormalised, p is the softmax over the choice alone (zero elsewhere);
 //   sigmoid: ds_j = dq_j q_j (1 - sigmoid(s_j)); renormalised q_j (dq_j - inner)(1 - sigmoid(s_j)).
 // The row is put together in LDS (dense term, then the choice's terms) and stored once.
-template <class T, int L, int E>
+template <class T, int L, int E, bool V>
 __global__ __launch_bounds__(kBlock) void k_route_grad(RouteGradArgs A) {
     constexpr int kSlots = kBlock / L;
+    using Rw = Row<T, L, E, V>;
+    using Elem = typename T::type;
     __shared__ float term[kSlots][kRouteMaxTop];
-    __shared__ int place[kSlots][kRouteMaxTop];
+    __shared__ int16_t place[kSlots][kRouteMaxTop];
     __shared__ float tile[kSlots][L * E];
     const int l = threadIdx.x % L, slot = threadIdx.x / L;
     const bool dense = !A.sigmoid && !A.renorm;
     for (int64_t i0 = (int64_t)blockIdx.x * kSlots; i0 < A.n; i0 += (int64_t)gridDim.x * kSlots) {
         const int64_t i = i0 + slot < A.n ? i0 + slot : i0;
         const bool on = i0 + slot < A.n;
-        const typename T::type* row = static_cast<const typename T::type*>(A.s) + i * A.ld;
+        const Elem* row = static_cast<const Elem*>(A.s) + i * A.ld;
         const int32_t* idx = A.idx + i * A.k;
         const float* dw = A.dw + i * A.k;
-        float s[E], M = kNegBig, S = 0.0f;
-        if (dense) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int j = e * L + l;
-                s[e] = T::to(row[j < A.m ? j : A.m - 1]);
-                if (j >= A.m) s[e] = -INFINITY;
-                M = fmaxf(M, s[e]);
+        // the choice: column (an entry outside the row was dropped: -1), score and gradient; the lane's first in registers
+        auto column = [&](int r) {
+            const int j = idx[r];
+            return (unsigned)j < (unsigned)A.m ? j : -1;
+        };
+        const int j0 = l < A.k ? column(l) : -1;
+        const float x0 = j0 >= 0 ? T::to(row[j0]) : -INFINITY, d0 = j0 >= 0 ? dw[l] : 0.0f;
+        auto each = [&](auto f) {
+            if (l < A.k) f(l, j0, x0, d0);
+            for (int r = l + L; r < A.k; r += L) {
+                const int j = column(r);
+                f(r, j, j >= 0 ? T::to(row[j]) : -INFINITY, dw[r]);
             }
+        };
+        float p[E], M = kNegBig, inv_S = 1.0f;
+        if (dense) {
+            Rw::load(row, l, A.m, p);
+            float S = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) M = fmaxf(M, p[e]);
             M = lanes_max<L>(M);
 #pragma unroll
-            for (int e = 0; e < E; ++e) S += exp_of(s[e] - M);
+            for (int e = 0; e < E; ++e) {
+                p[e] = exp_of(p[e] - M);
+                S += p[e];
+            }
             S = lanes_sum<L>(S);
-            if (S == 0.0f) S = 1.0f;
+            inv_S = S == 0.0f ? 1.0f : 1.0f / S;
         }
-        float top = kNegBig, sum = 0.0f, inner = 0.0f;
+        float shift = kNegBig, inv = 1.0f;
         if (A.renorm) {
-            for (int r = l; r < A.k; r += L) {
-                const int j = idx[r];
-                if ((unsigned)j >= (unsigned)A.m) continue;
-                const float x = T::to(row[j]);
-                top = fmaxf(top, act_exponent(A.sigmoid, x));
-            }
-            top = lanes_max<L>(top);
-            for (int r = l; r < A.k; r += L) {
-                const int j = idx[r];
-                if ((unsigned)j >= (unsigned)A.m) continue;
-                const float x = T::to(row[j]);
-                sum += act_shifted(A.sigmoid, x, top);
-            }
+            each([&](int, int, float x, float) { shift = fmaxf(shift, act_exponent(A.sigmoid, x)); });
+            shift = lanes_max<L>(shift);
+            float sum = 0.0f;
+            each([&](int, int, float x, float) { sum += act_shifted(A.sigmoid, x, shift); });
             sum = lanes_sum<L>(sum);
-            if (sum == 0.0f) sum = 1.0f;
+            inv = sum == 0.0f ? 1.0f : 1.0f / sum;
         }
-        for (int r = l; r < A.k; r += L) {
-            const int j = idx[r];
-            const bool in = (unsigned)j < (unsigned)A.m;  // an entry outside the row was dropped: no part
-            const float x = in ? T::to(row[j]) : -INFINITY;
-            float q = 0.0f;
-            if (in) {
-                if (A.renorm)
-                    q = act_shifted(A.sigmoid, x, top) / sum;
-                else
-                    q = A.sigmoid ? sigmoid_of(x) : exp_of(x - M) / S;
-            }
-            const float qd = in ? q * (A.scale * dw[r]) : 0.0f;
-            place[slot][r] = in ? j : -1;
+        auto weight = [&](float x) {  // q; 0 for a dropped entry (x = -inf)
+            return A.renorm ? act_shifted(A.sigmoid, x, shift) * inv : A.sigmoid ? sigmoid_of(x) : exp_of(x - M) * inv_S;
+        };
+        float inner = 0.0f;
+        each([&](int r, int j, float x, float d) {
+            const float qd = j >= 0 ? weight(x) * (A.scale * d) : 0.0f;
+            place[slot][r] = (int16_t)j;
             term[slot][r] = qd;
             inner += qd;
-        }
+        });
         inner = lanes_sum<L>(inner);
-        wave_sync();
+        const float all = dense ? -inv_S * inner : 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) tile[slot][e * L + l] = dense ? -(exp_of(s[e] - M) / S) * inner : 0.0f;
+        for (int e = 0; e < E; ++e) tile[slot][Rw::col(e, l)] = dense ? p[e] * all : 0.0f;
         wave_sync();
-        for (int r = l; r < A.k; r += L) {
-            const int j = place[slot][r];
-            if (j < 0) continue;
+        each([&](int r, int j, float x, float) {
+            if (j < 0) return;
             // an expert that stands twice in the row: its first entry takes the sum of all
             float total = 0.0f;
+            int copies = 0;
             bool first = true;
             for (int u = 0; u < A.k; ++u) {
                 if (place[slot][u] != j) continue;
                 if (u < r) first = false;
                 total += term[slot][u];
+                ++copies;
             }
-            if (!first) continue;
-            const float x = T::to(row[j]);
-            if (A.renorm) {
-                int copies = 0;
-                for (int u = 0; u < A.k; ++u) copies += place[slot][u] == j ? 1 : 0;
-                const float q = act_shifted(A.sigmoid, x, top) / sum;
-                total -= (float)copies * q * inner;
-            }
+            if (!first) return;
+            if (A.renorm) total -= (float)copies * weight(x) * inner;
             if (A.sigmoid) total *= sigmoid_of(-x);
             tile[slot][j] += total;
-        }
+        });
         wave_sync();
         if (on) {
-            typename T::type* out = static_cast<typename T::type*>(A.grad) + i * A.ldg;
+            float out[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int j = e * L + l;
-                if (j < A.m) out[j] = T::from(tile[slot][j]);
-            }
+            for (int e = 0; e < E; ++e) out[e] = tile[slot][Rw::col(e, l)];
+            Rw::store(static_cast<Elem*>(A.grad) + i * A.ldg, l, A.m, out);
         }
         wave_sync();
     }
@@ -654,7 +648,9 @@ template <class T>
 hipError_t launch_route_grad(const RouteGradArgs& A, hipStream_t s) {
     by_width(A.m, [&](auto lanes, auto per_lane) {
         constexpr int L = decltype(lanes)::value, E = decltype(per_lane)::value;
-        hipLaunchKernelGGL((k_route_grad<T, L, E>), dim3(route_grid(A.n, L)), dim3(kBlock), 0, s, A);
+        const bool runs = Row<T, L, E, true>::fits(A.s, A.ld, A.m) && Row<T, L, E, true>::fits(A.grad, A.ldg, A.m);
+        auto kernel = runs ? k_route_grad<T, L, E, true> : k_route_grad<T, L, E, false>;
+        hipLaunchKernelGGL(kernel, dim3(route_grid(A.n, L)), dim3(kBlock), 0, s, A);
     });
     return hipGetLastError();
 }
