@@ -25,18 +25,21 @@ namespace {
 struct F32 {
     using type = float;
     static constexpr uint32_t kNegInfBits = 0xff800000u;  // one 32-bit word of -inf elements
+    static constexpr int kLowBits = 0;                    // of the float32 value that are always zero
     __device__ static float to(float v) { return v; }
     __device__ static float from(float v) { return v; }
 };
 struct Bf16 {
     using type = uint16_t;
     static constexpr uint32_t kNegInfBits = 0xff80ff80u;
+    static constexpr int kLowBits = 16;
     __device__ static float to(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
     __device__ static uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }  // nearest even
 };
 struct F16 {
     using type = uint16_t;
     static constexpr uint32_t kNegInfBits = 0xfc00fc00u;
+    static constexpr int kLowBits = 13;
     __device__ static float to(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
     // Nearest even, of the float32 value: the product that made it is not contracted with the conversion, which the
     // compiler does in some of a kernel's paths and not in others.
@@ -109,6 +112,7 @@ struct OpMinU {
 // Sum over the 64 / L groups of L lanes of a wave (lanes with the same number in their groups), in every lane.
 template <int L>
 __device__ __forceinline__ float groups_sum(float x) {
+    asm("" : "+v"(x));  // (as in lanes_sum)
     uint32_t u = __builtin_bit_cast(uint32_t, x);
     OpAddF add;
     if constexpr (L <= 8) u = add(u, dpp<kRor8>(u));
@@ -126,9 +130,11 @@ template <int L>
 __device__ __forceinline__ float lanes_max(float x) {
     return __builtin_bit_cast(float, lanes_reduce<L>(__builtin_bit_cast(uint32_t, x), OpMaxF()));
 }
-// The order of the additions is fixed by the lane numbers alone.
+// The order of the additions is fixed by the lane numbers alone, and every lane gets the same bits: a product in x is
+// rounded first (contracted with the first addition, each lane would round only its neighbour's).
 template <int L>
 __device__ __forceinline__ float lanes_sum(float x) {
+    asm("" : "+v"(x));
     return __builtin_bit_cast(float, lanes_reduce<L>(__builtin_bit_cast(uint32_t, x), OpAddF()));
 }
 template <int L>
@@ -225,14 +231,19 @@ __device__ __forceinline__ double unordered(uint64_t k) {
     return __builtin_bit_cast(double, k ^ ((k >> 63) ? 0x8000000000000000ull : 0xffffffffffffffffull));
 }
 
-// The k-th largest of the 64 lanes' keys (the same in every lane).
-__device__ __forceinline__ uint32_t kth_of_wave(uint32_t key, int k) {
+// The k-th largest of the 64 lanes' N keys each (the same in every lane), 0 if they are fewer.  LOW: the lowest
+// bits that are all alike in every key, 0 above the sign's and 1 below it (ordered keys of 16-bit scores).
+template <int LOW, int N>
+__device__ __forceinline__ uint32_t kth_of_wave(const uint32_t (&key)[N], int k) {
     uint32_t t = 0;
-    for (int b = 31; b >= 0; --b) {
+    for (int b = 31; b >= LOW; --b) {
         const uint32_t x = t | (1u << b);
-        if (__popcll(__ballot(key >= x)) >= k) t = x;
+        int have = 0;
+#pragma unroll
+        for (int c = 0; c < N; ++c) have += __popcll(__ballot(key[c] >= x));
+        if (have >= k) t = x;
     }
-    return t;
+    return LOW > 0 && t && !(t >> 31) ? t | ((1u << LOW) - 1) : t;
 }
 
 // ----- host-side checks ---------------------------------------------------------------

@@ -5,16 +5,20 @@
 // With z = s / eps and M = max_j s_j, S = sum_j exp((s_j - M)/eps) of a row,
 //     lse = M/eps + log S,   log p_j = (s_j - M)/eps - log S,
 //     H = -sum_j p_j log p_j = log S - (sum_j e_j d_j) / S,  d = (s - M)/eps, e = exp(d).
-// The scores are read once.  A workgroup holds a chunk of a row in registers
-// (16-byte loads), so the maximum is known before the sum and nothing is
-// rescaled; longer rows are cut into chunks whose (M, S, sum e d) and sorted
-// candidate lists a second kernel joins.
+// The scores are read once: a thread keeps a running maximum and rescales its
+// sums once per block of four 16-byte loads.  Rows are cut only where there are too few to
+// fill the GPU, or where a row has more blocks than LDS has room for; a second
+// kernel joins the cuts' (M, S, sum e d) and sorted lists of their largest entries.
 //
-// The largest entries of a chunk: the maximum of every lane number over the
-// workgroup's waves gives 64 disjoint classes; the k-th largest of their
-// maxima is at most the k-th largest score, so only entries above it (about
-// k + k^2 / 100 of them) and the first ones equal to it are candidates, whose ranks are
-// counted in LDS.  Ties go to the lowest index.
+// The largest entries: every thread leaves the maximum of each of its blocks in
+// LDS.  The threads (in rows that a wave takes alone, its threads' blocks) are
+// classes of entries; the k-th largest of the classes' maxima is at most the
+// k-th largest score, so only blocks that reach it are looked at again, and of
+// their entries only those above it (with 256 classes 21 at k = 20, 74 at k = 64 in
+// the mean) and the first ones equal to it are candidates, whose ranks are counted.
+// Ties go to the lowest column.  Where the largest entries crowd into few
+// classes, or more entries equal the bound than the list holds, the cut is read
+// again.
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -24,7 +28,9 @@ namespace {
 
 constexpr int kMaxTop = 64;
 constexpr int64_t kTopMaxCols = (int64_t)1 << 20;  // columns, where alternatives are asked for
-constexpr int64_t kLpGrid = 1 << 20;               // workgroups of one launch (each may serve several chunks)
+constexpr int64_t kLpGrid = 1 << 20;               // workgroups of one launch (each may serve several rows)
+constexpr int kLpVecs = 4;                         // 16-byte loads of a thread's block
+constexpr int kLpBlocks = 32;                      // blocks whose maxima LDS holds: 32 KB
 
 struct LpArgs {
     const void* s;
@@ -36,6 +42,7 @@ struct LpArgs {
     float *logp, *lse, *entropy, *top_logp, *stats;
     int32_t* top_idx;
     int splits;
+    int cut;  // vectors of 16 bytes in a cut of k_logprobs_stream
     // partial results of the chunks, [n * splits] each, lists [n * splits][top]
     float *pm, *ps, *px;
     uint64_t* plist;
@@ -45,9 +52,23 @@ struct LpArgs {
 __device__ __forceinline__ uint64_t cand(float v, uint32_t j) { return (uint64_t)ordered(v) << 32 | (uint32_t)~j; }
 __device__ __forceinline__ uint32_t cand_col(uint64_t k) { return ~(uint32_t)k; }
 
-// The row's outputs from its maximum and sums.  Called by one lane.
+// The row's target and its score, loaded ahead of the sums they are needed after.  Called by one lane.
+struct Target {
+    int64_t t;
+    float s;
+};
 template <class T>
-__device__ void finish_row(const LpArgs& A, int64_t i, float M, float S, float X) {
+__device__ __forceinline__ Target load_target(const LpArgs& A, int64_t i) {
+    Target g{-1, 0.0f};
+    if (A.targets) {
+        g.t = A.targets[i];
+        if (g.t >= 0 && g.t < A.m) g.s = T::to(static_cast<const typename T::type*>(A.s)[i * A.ld + g.t]);
+    }
+    return g;
+}
+
+// The row's outputs from its maximum and sums.  Called by one lane.
+__device__ __forceinline__ void finish_row(const LpArgs& A, int64_t i, const Target& g, float M, float S, float X) {
     const bool empty = S == 0.0f;
     const float top = empty ? -INFINITY : M;
     const float log_s = empty ? 0.0f : logf(S);
@@ -59,29 +80,26 @@ __device__ void finish_row(const LpArgs& A, int64_t i, float M, float S, float X
         A.entropy[i] = empty || h < 0.0f ? 0.0f : h;
     }
     if (A.targets) {
-        const int64_t t = A.targets[i];
         float lp = 0.0f;  // no token given
-        if (t >= A.m)
+        if (g.t >= A.m)
             lp = NAN;
-        else if (t >= 0)
-            lp = empty ? -INFINITY : (T::to(static_cast<const typename T::type*>(A.s)[i * A.ld + t]) - M) / A.eps - log_s;
+        else if (g.t >= 0)
+            lp = empty ? -INFINITY : (g.s - M) / A.eps - log_s;
         A.logp[i] = lp;
     }
 }
 
-template <class T>
+// (The key holds the score; a NaN's says -inf, but then S is NaN.)
 __device__ __forceinline__ void finish_top(const LpArgs& A, int64_t i, int r, uint64_t key, float M, float S) {
-    const uint32_t j = cand_col(key);
-    const float s = T::to(static_cast<const typename T::type*>(A.s)[i * A.ld + j]);
-    A.top_idx[i * A.top + r] = (int32_t)j;
-    A.top_logp[i * A.top + r] = S == 0.0f ? -INFINITY : (s - M) / A.eps - logf(S);
+    A.top_idx[i * A.top + r] = (int32_t)cand_col(key);
+    A.top_logp[i * A.top + r] = S == 0.0f ? -INFINITY : (unordered((uint32_t)(key >> 32)) - M) / A.eps - logf(S);
 }
 
 template <class T>
 struct Vec {
     static constexpr int n = 16 / sizeof(typename T::type);
     uint4 raw;
-    __device__ float at(int i) const {
+    __device__ __forceinline__ float at(int i) const {
         if constexpr (n == 4) {
             const uint32_t w = i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w;
             return __builtin_bit_cast(float, w);
@@ -92,268 +110,352 @@ struct Vec {
     }
 };
 
-// One chunk of a row per workgroup of W waves: NV 16-byte vectors per thread.
-// The first chunk also takes the row's few entries before the first and after
-// the last aligned 16 bytes, one per thread.
-template <class T, int W, int NV>
-__global__ __launch_bounds__(W * 64) void k_logprobs(LpArgs A) {
-    constexpr int kThreads = W * 64, VE = Vec<T>::n;
-    constexpr int kCap = W == 1 ? 256 : 1024;  // candidates above the threshold
-    __shared__ uint64_t list[kCap + W * kMaxTop];
-    __shared__ float red[W][3];
-    __shared__ uint32_t lane_max[W][64];
-    __shared__ uint32_t shared_t;
-    __shared__ int count;
+// Joins the (M, S, X) of lanes or waves: sums relative to the common maximum top.
+__device__ __forceinline__ void rescale(float M, float top, float c, float& S, float& X) {
+    const float d = fmaxf((M - top) * c, -16384.0f), w = s_ex2(d);
+    X = w * fmaf(S, d, X);
+    S *= w;
+}
+
+// The k-th largest of the classes' maxima: of all W * 64 threads', or, for small k, of the 64 lane numbers', which
+// takes W times fewer steps and leaves about k^2 / 128 entries more (measured alike at k = 24).
+template <int LOW, int W>
+__device__ __forceinline__ uint32_t kth_of_classes(const uint32_t (*class_max)[64], int lane, int k) {
+    uint32_t key[W], most[1] = {0};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        key[w] = class_max[w][lane];
+        most[0] = max(most[0], key[w]);
+    }
+    return k <= 24 ? kth_of_wave<LOW>(most, k) : kth_of_wave<LOW>(key, k);
+}
+
+// A row, or a cut of one, per W waves (4 / W rows per workgroup).  Dynamic LDS with TOP: the blocks' maxima,
+// [blocks][256].
+template <class T, int W, int NV, bool ENT, bool TOP>
+__global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs A) {
+    constexpr int VE = Vec<T>::n, kThreads = W * 64, kRows = kBlock / kThreads, kStep = kThreads * NV;
+    constexpr int kCap = W == 1 ? 704 : 1024;                  // candidates above the bound
+    constexpr int kEqual = W * kMaxTop, kHits = TOP ? 512 : 1;  // entries equal to it; blocks that reach it
+    __shared__ float red[kBlock / 64][3];
+    __shared__ uint32_t class_max[TOP ? kBlock / 64 : 1][64];
+    __shared__ uint64_t lists[TOP ? kRows : 1][TOP ? kCap + kEqual : 1];
+    __shared__ uint16_t hit_lists[TOP ? kRows : 1][kHits];
+    __shared__ int counts[kRows][3];
+    extern __shared__ float block_max[];
     using E = typename T::type;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
-    for (int64_t item = blockIdx.x; item < A.n * A.splits; item += gridDim.x) {
-        const int64_t i = item / A.splits;
-        const int split = (int)(item % A.splits);
+    const int t = threadIdx.x % kThreads, lane = threadIdx.x & 63, wave = threadIdx.x / 64, slot = threadIdx.x / kThreads;
+    auto sync = [] {
+        if constexpr (W == 1)
+            wave_sync();
+        else
+            __syncthreads();
+    };
+    const int64_t items = A.n * A.splits;
+    for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items; item0 += (int64_t)gridDim.x * kRows) {
+        const int64_t item = item0 + slot;
+        const bool on = item < items;
+        const int64_t i = (on ? item : item0) / A.splits;
+        const int split = (int)((on ? item : item0) - i * A.splits);
         const E* row = static_cast<const E*>(A.s) + i * A.ld;
         const int mis = (int)(reinterpret_cast<uintptr_t>(row) / sizeof(E) % VE);
         const int head = min(A.m, (VE - mis) % VE);
         const int vecs = (A.m - head) / VE, tail = A.m - head - vecs * VE;
-        const int v0 = split * (kThreads * NV);
-        const E* body = row + head;
-        Vec<T> v[NV];
-        float x = -INFINITY;
-        int xj = -1;  // column of the single entry
+        const int v0 = split * A.cut, v1 = min(vecs, v0 + A.cut);
+        const uint4* body = reinterpret_cast<const uint4*>(row + head);
+        const int blocks = v1 > v0 ? (v1 - v0 + kStep - 1) / kStep : 0;
+        Target target{-1, 0.0f};
+        if (t == 0 && A.splits == 1) target = load_target<T>(A, i);
+        Vec<T> next[NV], v[NV];
+        auto fetch = [&](int b) {
 #pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            const int at = v0 + q * kThreads + tid;
-            v[q].raw = make_uint4(T::kNegInfBits, T::kNegInfBits, T::kNegInfBits, T::kNegInfBits);
-            if (at < vecs) v[q].raw = *reinterpret_cast<const uint4*>(body + (int64_t)at * VE);
+            for (int q = 0; q < NV; ++q) next[q].raw = body[min(v0 + b * kStep + q * kThreads + t, v1 - 1)];
+        };
+        if (blocks > 0) fetch(0);
+        float M = kNegBig, S = 0.0f, X = 0.0f, single = -INFINITY, largest = -INFINITY;  // (M starts above -inf)
+        int single_j = -1;
+        if (split == 0 && t < head + tail) {  // the row's single entries, one per thread
+            single_j = t < head ? t : vecs * VE + t;
+            single = T::to(row[single_j]);
+            M = fmaxf(M, single);
+            largest = fmaxf(largest, single);
+            const float d = (single - M) * A.c;
+            S = s_ex2(d);
+            X = S * fmaxf(d, -16384.0f);
         }
-        if (split == 0) {
-            if (tid < head)
-                xj = tid;
-            else if (tid < head + tail)
-                xj = vecs * VE + tid;
-            if (xj >= 0) x = T::to(row[xj]);
-        }
-        // maximum
-        float vm[NV], tm = x;
+        for (int b = 0; b < blocks; ++b) {
 #pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            vm[q] = v[q].at(0);
+            for (int q = 0; q < NV; ++q) v[q] = next[q];
+            if (b + 1 < blocks) {
+                fetch(b + 1);
+            } else {  // vectors behind the end
 #pragma unroll
-            for (int e = 1; e < VE; ++e) vm[q] = fmaxf(vm[q], v[q].at(e));
-            tm = fmaxf(tm, vm[q]);
-        }
-        if (A.top) lane_max[wave][lane] = ordered(tm);
-        const float wm = lanes_max<64>(tm);
-        if (lane == 0) red[wave][0] = wm;
-        if (tid == 0) count = 0;
-        __syncthreads();
-        float M = kNegBig;
-        for (int w = 0; w < W; ++w) M = fmaxf(M, red[w][0]);
-        if (A.top && wave == 0) {
-            uint32_t k = lane_max[0][lane];
-            for (int w = 1; w < W; ++w) k = max(k, lane_max[w][lane]);
-            k = kth_of_wave(k, A.top);
-            if (lane == 0) shared_t = k;
-        }
-        // sums; an entry of -inf adds nothing
-        float S = 0.0f, X = 0.0f;
-        if (A.entropy) {
+                for (int q = 0; q < NV; ++q)
+                    if (v0 + b * kStep + q * kThreads + t >= v1)
+                        v[q].raw = make_uint4(T::kNegInfBits, T::kNegInfBits, T::kNegInfBits, T::kNegInfBits);
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) top = fmaxf(top, v[q].at(e));
+            if (TOP) {
+                block_max[b * kBlock + threadIdx.x] = top;
+                largest = fmaxf(largest, top);
+            }
+            top = fmaxf(M, top);
+            rescale(M, top, A.c, S, X);
+            M = top;
+            float s = 0.0f, x = 0.0f;
 #pragma unroll
             for (int q = 0; q < NV; ++q)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
                     const float d = (v[q].at(e) - M) * A.c, ex = s_ex2(d);
-                    S += ex;
-                    X = fmaf(ex, fmaxf(d, -16384.0f), X);
+                    s += ex;
+                    if (ENT) x = fmaf(ex, fmaxf(d, -16384.0f), x);  // an entry of -inf adds nothing
                 }
-            const float d = (x - M) * A.c, ex = s_ex2(d);
-            S += ex;
-            X = fmaf(ex, fmaxf(d, -16384.0f), X);
-        } else {
-#pragma unroll
-            for (int q = 0; q < NV; ++q)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) S += s_ex2((v[q].at(e) - M) * A.c);
-            S += s_ex2((x - M) * A.c);
+            S += s;
+            X += x;
         }
-        S = lanes_sum<64>(S);
-        X = lanes_sum<64>(X);
-        if (lane == 0) red[wave][1] = S, red[wave][2] = X;
-        __syncthreads();
-        S = X = 0.0f;
-        for (int w = 0; w < W; ++w) S += red[w][1], X += red[w][2];
-
-        if (tid == 0) {
-            if (A.splits == 1)
-                finish_row<T>(A, i, M, S, X);
-            else
-                A.pm[item] = M, A.ps[item] = S, A.px[item] = X;
-        }
-        if (A.top) {
-            const uint32_t t = shared_t;
-            const int jv = head + (v0 + tid) * VE;  // column of the thread's first entry
-            // entries above the threshold, in any order
-            if (__any(ordered(tm) > t)) {
-                if (xj >= 0 && ordered(x) > t) {
-                    const int at = atomicAdd(&count, 1);
-                    if (at < kCap) list[at] = cand(x, xj);
-                }
-#pragma unroll
-                for (int q = 0; q < NV; ++q) {
-                    if (!__any(ordered(vm[q]) > t)) continue;
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const float s = v[q].at(e);
-                        if (ordered(s) > t) {
-                            const int at = atomicAdd(&count, 1);
-                            if (at < kCap) list[at] = cand(s, jv + q * kThreads * VE + e);
-                        }
-                    }
-                }
-            }
+        float top = lanes_max<64>(M);
+        if (TOP) class_max[wave][lane] = blocks > 0 || single_j >= 0 ? ordered(largest) : 0u;
+        if (TOP && t == 0) counts[slot][0] = counts[slot][1] = counts[slot][2] = 0;
+        if (W > 1) {
+            if (lane == 0) red[wave][0] = top;
             __syncthreads();
-            int have = count;
-            uint64_t* out = A.splits == 1 ? nullptr : A.plist + item * A.top;
-            if (have <= kCap) {
-                // the first entries equal to the threshold: each wave its own first ones, in order of the column
-                const int need = A.top - have;
-                int mine = 0;  // found by this wave
-                if (need > 0) {
-                    uint64_t* eq = list + have + wave * need;
-                    const uint64_t below = (1ull << lane) - 1;
-                    // the single entries: the ones before the vectors come first, the ones after them last
-                    for (int part = 0; part < 3; ++part) {
-                        if (part == 1) {
 #pragma unroll
-                            for (int q = 0; q < NV; ++q) {
-                                const bool in = v0 + q * kThreads + tid < vecs;
-                                if (mine >= need || !__any(in && ordered(vm[q]) >= t)) continue;
-                                uint32_t hit = 0;
-                                int before = 0, total = 0;
+            for (int w = 0; w < W; ++w) top = fmaxf(top, red[w][0]);
+        }
+        rescale(M, top, A.c, S, X);
+        S = lanes_sum<64>(S);
+        if (ENT) X = lanes_sum<64>(X);
+        if (W > 1) {
+            if (lane == 0) red[wave][1] = S, red[wave][2] = X;
+            __syncthreads();
+            S = X = 0.0f;
 #pragma unroll
-                                for (int e = 0; e < VE; ++e) {
-                                    const bool h = in && ordered(v[q].at(e)) == t;
-                                    const uint64_t mask = __ballot(h);
-                                    hit |= h ? 1u << e : 0u;
-                                    before += __popcll(mask & below);
-                                    total += __popcll(mask);
-                                }
-                                int at = mine + before;
-#pragma unroll
-                                for (int e = 0; e < VE; ++e)
-                                    if (hit >> e & 1) {
-                                        if (at < need) eq[at] = cand(v[q].at(e), jv + q * kThreads * VE + e);
-                                        ++at;
-                                    }
-                                mine += total;
-                            }
-                        } else if (wave == 0 && split == 0 && mine < need) {
-                            const bool h = xj >= 0 && (part == 0) == (xj < head) && ordered(x) == t;
-                            const uint64_t mask = __ballot(h);
-                            const int at = mine + __popcll(mask & below);
-                            if (h && at < need) eq[at] = cand(x, xj);
-                            mine += __popcll(mask);
-                        }
-                    }
-                    mine = min(mine, need);
-                    // close the gaps between the waves' entries with keys that rank last
-                    for (int at = mine + lane; at < need; at += 64) eq[at] = 0;
-                    have += W * need;
+            for (int w = 0; w < W; ++w) S += red[w][1], X += red[w][2];
+        }
+        if (t == 0 && on) {
+            if (A.splits == 1)
+                finish_row(A, i, target, top, S, X);
+            else
+                A.pm[item] = top, A.ps[item] = S, A.px[item] = X;
+        }
+        if constexpr (TOP) {
+            if (W == 1) wave_sync();
+            uint64_t* list = lists[slot];
+            uint16_t* hits = hit_lists[slot];
+            int* count = counts[slot];  // candidates above the bound, blocks that reach it, entries that equal it
+            uint32_t bound;
+            if constexpr (W == 1) {
+                const float second = blocks > 1 ? block_max[kBlock + threadIdx.x] : -INFINITY;
+                const uint32_t first = blocks > 1 ? ordered(fmaxf(block_max[threadIdx.x], single)) : class_max[wave][lane];
+                const uint32_t key[2] = {first, blocks > 1 ? ordered(second) : 0u};
+                bound = kth_of_wave<T::kLowBits>(key, A.top);
+            } else {
+                bound = kth_of_classes<T::kLowBits, W>(class_max, lane, A.top);
+            }
+            // a mask that leaves fewer classes than k: the entries equal to the bound are the masked ones
+            const bool masked = bound <= ordered(-INFINITY);
+            auto column = [&](int at, int e) { return (uint32_t)(head + at * VE + e); };
+            auto see = [&](float s, uint32_t j, bool equals) {
+                const uint32_t k = ordered(s);
+                if (k > bound) {
+                    const int at = atomicAdd(&count[0], 1);
+                    if (at < kCap) list[at] = cand(s, j);
+                } else if (equals && k == bound) {
+                    const int at = atomicAdd(&count[2], 1);
+                    if (at < kEqual) list[kCap + at] = cand(s, j);
                 }
-                __syncthreads();
-                for (int a = tid; a < have; a += kThreads) {
-                    const uint64_t key = list[a];
-                    int rank = 0;
-                    for (int b = 0; b < have; ++b) rank += list[b] > key ? 1 : 0;
-                    if (key && rank < A.top) {
-                        if (out)
-                            out[rank] = key;
-                        else
-                            finish_top<T>(A, i, rank, key, M, S);
-                    }
+            };
+            if (single_j >= 0) see(single, (uint32_t)single_j, true);
+            for (int b = 0; b < blocks; ++b)
+                if (ordered(block_max[b * kBlock + threadIdx.x]) >= bound + (masked ? 1 : 0)) {
+                    const int at = atomicAdd(&count[1], 1);
+                    if (at < kHits) hits[at] = (uint16_t)(b * kThreads + t);
                 }
-                // a chunk with fewer entries than asked for (only a cut row has one): the rest ranks last
-                if (out) {
-                    int found = 0;
-                    for (int b = lane; b < have; b += 64) found += list[b] ? 1 : 0;
-                    for (int o = 1; o < 64; o *= 2) found += __shfl_xor(found, o);
-                    for (int r = found + tid; r < A.top; r += kThreads) out[r] = 0;
+            sync();
+            const int reached = count[1];
+            if (reached <= kHits) {
+                for (int h = t; h < reached * NV; h += kThreads) {
+                    const int hit = hits[h / NV], at = v0 + hit / kThreads * kStep + h % NV * kThreads + hit % kThreads;
+                    if (at >= v1) continue;
+                    Vec<T> x;
+                    x.raw = body[at];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) see(x.at(e), column(at, e), !masked);
                 }
             } else {
-                // the largest entries crowd into a few lane classes: one round of the workgroup for each
+                for (int at = v0 + t; at < v1; at += kThreads) {
+                    Vec<T> x;
+                    x.raw = body[at];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) see(x.at(e), column(at, e), false);
+                }
+            }
+            sync();
+            const int above = count[0], equal = count[2];
+            uint64_t* out = A.splits == 1 ? nullptr : A.plist + (on ? item : item0) * A.top;
+            auto place = [&](int rank, uint64_t key) {
+                if (!on) return;
+                if (out)
+                    out[rank] = key;
+                else
+                    finish_top(A, i, rank, key, top, S);
+            };
+            if (above <= kCap) {
+                const int need = A.top - above;
+                int have = above;
+                if (need > 0 && !masked && reached <= kHits && equal <= kEqual) {
+                    for (int a = t; a < equal; a += kThreads) {
+                        const uint64_t key = list[kCap + a];  // moved up behind the others; kCap is far behind them
+                        list[above + a] = key;
+                    }
+                    have = above + equal;
+                } else if (need > 0) {
+                    // masked ones, or more than the list holds: each wave its own first ones, in order of the column
+                    uint64_t* eq = list + above + (wave % W) * need;
+                    const uint64_t below = (1ull << lane) - 1;
+                    int mine = 0;
+                    auto take = [&](bool hit, uint64_t key, int before, int total) {
+                        if (hit && mine + before < need) eq[mine + before] = key;
+                        mine += total;
+                    };
+                    auto take_single = [&](bool in) {
+                        const bool hit = in && ordered(single) == bound;
+                        const uint64_t mask = __ballot(hit);
+                        take(hit, cand(single, (uint32_t)single_j), __popcll(mask & below), __popcll(mask));
+                    };
+                    take_single(single_j >= 0 && single_j < head);
+                    for (int at0 = v0 + (wave % W) * 64; at0 < v1 && mine < need; at0 += kThreads) {
+                        const int at = at0 + lane;
+                        Vec<T> x;
+                        x.raw = body[min(at, v1 - 1)];
+                        uint32_t hit = 0;
+                        int before = 0, total = 0;
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            const bool h = at < v1 && ordered(x.at(e)) == bound;
+                            const uint64_t mask = __ballot(h);
+                            hit |= h ? 1u << e : 0u;
+                            before += __popcll(mask & below);
+                            total += __popcll(mask);
+                        }
+                        int to = mine + before;
+#pragma unroll
+                        for (int e = 0; e < VE; ++e)
+                            if (hit >> e & 1) {
+                                if (to < need) eq[to] = cand(x.at(e), column(at, e));
+                                ++to;
+                            }
+                        mine += total;
+                    }
+                    if (mine < need) take_single(single_j >= head);
+                    for (int at = min(mine, need) + lane; at < need; at += 64) eq[at] = 0;  // ranks last
+                    have = above + W * need;
+                }
+                sync();
+                int found = 0;
+                for (int a = t; a < have; a += kThreads) {
+                    const uint64_t key = list[a];
+                    int rank = 0;
+#pragma unroll 4
+                    for (int b = 0; b < have; ++b) rank += list[b] > key ? 1 : 0;
+                    if (key && rank < A.top) place(rank, key);
+                }
+                if (out) {  // a cut with fewer entries than asked for: the rest ranks last
+                    for (int b = lane; b < have; b += 64) found += list[b] ? 1 : 0;
+                    found = (int)lanes_sum_u<64>((uint32_t)found);
+                    for (int r = found + t; r < A.top; r += kThreads) place(r, 0);
+                }
+            } else {
+                // the largest entries crowd into a few classes: one reading of the cut for each
                 uint64_t last = ~0ull;
                 for (int r = 0; r < A.top; ++r) {
                     uint64_t best = 0;
-                    if (xj >= 0) {
-                        const uint64_t k = cand(x, xj);
-                        best = k < last ? k : 0;
+                    auto look = [&](uint64_t k) { best = k < last && k > best ? k : best; };
+                    if (single_j >= 0) look(cand(single, (uint32_t)single_j));
+                    for (int at = v0 + t; at < v1; at += kThreads) {
+                        Vec<T> x;
+                        x.raw = body[at];
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) look(cand(x.at(e), column(at, e)));
                     }
-#pragma unroll
-                    for (int q = 0; q < NV; ++q)
-                        if (v0 + q * kThreads + tid < vecs) {
-#pragma unroll
-                            for (int e = 0; e < VE; ++e) {
-                                const uint64_t k = cand(v[q].at(e), jv + q * kThreads * VE + e);
-                                best = k < last && k > best ? k : best;
-                            }
-                        }
                     const uint32_t hi = lanes_max<64>((uint32_t)(best >> 32));
                     const uint32_t lo = lanes_max<64>((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-                    if (lane == 0) list[wave] = (uint64_t)hi << 32 | lo;
-                    __syncthreads();
-                    best = list[0];
-                    for (int w = 1; w < W; ++w) best = max(best, list[w]);
-                    if (tid == 0) {
-                        if (out)
-                            out[r] = best;
-                        else
-                            finish_top<T>(A, i, r, best, M, S);
+                    best = (uint64_t)hi << 32 | lo;
+                    if (W > 1) {
+                        if (lane == 0) list[wave] = best;
+                        __syncthreads();
+#pragma unroll
+                        for (int w = 0; w < W; ++w) best = max(best, list[w]);
+                        __syncthreads();
                     }
+                    if (t == 0) place(r, best);
                     last = best;
-                    __syncthreads();
                 }
             }
+            sync();
         }
-        __syncthreads();
     }
 }
 
-// Joins the chunks of a cut row: one workgroup per row.
-template <class T>
+// Joins the chunks of a cut row: one wave per row, or (TOP) one workgroup.
+template <class T, bool TOP>
 __global__ __launch_bounds__(kBlock) void k_logprobs_join(LpArgs A) {
-    extern __shared__ uint64_t list[];  // [splits][top]
-    __shared__ float red[kBlock / 64][2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
-    for (int64_t i = blockIdx.x; i < A.n; i += gridDim.x) {
+    constexpr int kWaves = TOP ? kBlock / 64 : 1, kRows = kBlock / 64 / kWaves;
+    extern __shared__ uint64_t list[];  // [splits][top] entries, then those near the top
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < A.n; i0 += (int64_t)gridDim.x * kRows) {
+        const int64_t i = min(i0 + (TOP ? 0 : tid / 64), A.n - 1);
         const int64_t p0 = i * A.splits;
-        float M = kNegBig;
-        for (int k = tid; k < A.splits; k += kBlock) M = fmaxf(M, A.pm[p0 + k]);
-        M = lanes_max<64>(M);
-        if (lane == 0) red[wave][0] = M;
-        __syncthreads();
-        for (int w = 0; w < kBlock / 64; ++w) M = fmaxf(M, red[w][0]);
-        __syncthreads();
-        float S = 0.0f, X = 0.0f;
-        for (int k = tid; k < A.splits; k += kBlock) {
-            const float s = A.ps[p0 + k], d = (A.pm[p0 + k] - M) * A.c, w = s_ex2(d);
-            if (s == 0.0f) continue;
-            S = fmaf(s, w, S);
-            X = fmaf(w, fmaf(s, fmaxf(d, -16384.0f), A.px[p0 + k]), X);
+        const Target target = load_target<T>(A, i);
+        const int total = A.splits * A.top;
+        if (TOP)
+            for (int a = tid; a < total; a += kBlock) list[a] = A.plist[p0 * A.top + a];
+        // every wave joins the sums for itself
+        float M = kNegBig, S = 0.0f, X = 0.0f;
+        for (int k = lane; k < A.splits; k += 64) {
+            const float m = A.pm[p0 + k], s = A.ps[p0 + k], x = A.px[p0 + k], top = fmaxf(M, m);
+            float s1 = s, x1 = x;
+            rescale(m, top, A.c, s1, x1);
+            rescale(M, top, A.c, S, X);
+            S += s1;
+            X += x1;
+            M = top;
         }
+        const float top = lanes_max<64>(M);
+        rescale(M, top, A.c, S, X);
         S = lanes_sum<64>(S);
         X = lanes_sum<64>(X);
-        if (lane == 0) red[wave][0] = S, red[wave][1] = X;
-        const int total = A.splits * A.top;
-        for (int a = tid; a < total; a += kBlock) list[a] = A.plist[p0 * A.top + a];
-        __syncthreads();
-        S = X = 0.0f;
-        for (int w = 0; w < kBlock / 64; ++w) S += red[w][0], X += red[w][1];
-        if (tid == 0) finish_row<T>(A, i, M, S, X);
-        for (int a = tid; a < total; a += kBlock) {
-            const uint64_t key = list[a];
-            int rank = 0;
-            for (int b = 0; b < total; ++b) rank += list[b] > key ? 1 : 0;
-            if (key && rank < A.top) finish_top<T>(A, i, rank, key, M, S);
+        if (TOP ? tid == 0 : lane == 0 && i0 + tid / 64 < A.n) finish_row(A, i, target, top, S, X);
+        if constexpr (TOP) {
+            // as in k_logprobs: the entries' upper halves reach the k-th largest thread's maximum, then ranks
+            __shared__ uint32_t class_max[kBlock / 64][64];
+            __shared__ int count;
+            if (tid == 0) count = 0;
+            __syncthreads();
+            uint32_t most = 0;
+            for (int a = tid; a < total; a += kBlock) most = max(most, (uint32_t)(list[a] >> 32));
+            class_max[tid / 64][lane] = most;
+            __syncthreads();
+            const uint32_t bound = max(kth_of_classes<T::kLowBits, kBlock / 64>(class_max, lane, A.top), 1u);  // (0: no entry)
+            uint64_t* near = list + total;
+            for (int a = tid; a < total; a += kBlock)
+                if ((uint32_t)(list[a] >> 32) >= bound) near[atomicAdd(&count, 1)] = list[a];
+            __syncthreads();
+            const int have = count;
+            for (int a = tid; a < have; a += kBlock) {
+                const uint64_t mine = near[a];
+                int rank = 0;
+#pragma unroll 4
+                for (int b = 0; b < have; ++b) rank += near[b] > mine ? 1 : 0;
+                if (rank < A.top) finish_top(A, i, rank, mine, top, S);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -487,19 +589,37 @@ int64_t chunks(int64_t m, int es, int vecs) {
     return std::max<int64_t>(1, (v + vecs - 1) / vecs);
 }
 
-constexpr int kLpWide = 8 * 64 * 8;  // vectors of the widest chunk
+// How a forward pass cuts its rows: whole where there are kFill of them, else to make kFill pieces, none below kCutMin
+// vectors.  With alternatives a piece has at most kLpBlocks blocks, and a row no more pieces than
+// the joining workgroup ranks the lists of, kJoin entries, where that leaves pieces of kLpBlocks.
+constexpr int kFill = 1024, kCutMin = 1024, kJoin = 1024;
 
-int64_t lp_splits(int64_t m, int es) { return chunks(m, es, kLpWide); }
+struct LpCut {
+    int64_t splits;
+    int cut;
+};
+
+LpCut lp_cut(int es, int64_t n, int64_t m, int top) {
+    const int64_t vecs = std::max<int64_t>(1, m * es / 16);
+    int64_t most = std::min((kFill + n - 1) / std::max<int64_t>(n, 1), vecs / kCutMin);
+    if (top > 0) {
+        const int64_t longest = (int64_t)kLpBlocks * kLpVecs * kBlock;
+        most = std::max(std::min<int64_t>(most, kJoin / top), (vecs + longest - 1) / longest);
+    }
+    most = std::max<int64_t>(1, most);
+    const int64_t cut = (vecs + most - 1) / most;
+    return {(vecs + cut - 1) / cut, (int)cut};
+}
 
 struct LpLayout {
-    int64_t splits;
+    LpCut cut;
     size_t pm, ps, px, plist, total;
 };
 
 LpLayout lp_layout(int es, int64_t n, int64_t m, int top) {
-    LpLayout L{lp_splits(m, es), 0, 0, 0, 0, 256};
-    if (L.splits == 1) return L;
-    const size_t items = (size_t)n * (size_t)L.splits;
+    LpLayout L{lp_cut(es, n, m, top), 0, 0, 0, 0, 256};
+    if (L.cut.splits == 1) return L;
+    const size_t items = (size_t)n * (size_t)L.cut.splits;
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     L.ps = up(items * 4);
     L.px = L.ps + up(items * 4);
@@ -509,26 +629,34 @@ LpLayout lp_layout(int es, int64_t n, int64_t m, int top) {
 }
 
 template <class T, int W, int NV>
-void launch_lp(const LpArgs& A, hipStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>(A.n * A.splits, kLpGrid);
-    hipLaunchKernelGGL((k_logprobs<T, W, NV>), dim3(grid), dim3(W * 64), 0, s, A);
+void launch_rows(const LpArgs& A, hipStream_t s) {
+    const int rows = kBlock / (W * 64);
+    const unsigned grid = (unsigned)std::min<int64_t>((A.n * A.splits + rows - 1) / rows, kLpGrid);
+    auto kernel = A.top ? (A.entropy ? k_logprobs<T, W, NV, true, true> : k_logprobs<T, W, NV, false, true>)
+                        : (A.entropy ? k_logprobs<T, W, NV, true, false> : k_logprobs<T, W, NV, false, false>);
+    const int step = W * 64 * NV;
+    const size_t lds = A.top ? (size_t)((A.cut + step - 1) / step) * kBlock * sizeof(float) : 0;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kBlock), lds, s, A);
 }
 
 template <class T>
 hipError_t logprobs(const LpArgs& A, hipStream_t s) {
+    // a wave takes a row alone up to two blocks (512 vectors), with one vector per lane where that is all of it
     const int64_t vecs = A.m * (int64_t)sizeof(typename T::type) / 16;
-    if (vecs <= 64 * 2)
-        launch_lp<T, 1, 2>(A, s);
-    else if (vecs <= 64 * 8)
-        launch_lp<T, 1, 8>(A, s);
-    else if (vecs <= 512 * 2)
-        launch_lp<T, 8, 2>(A, s);
+    if (vecs <= 64)
+        launch_rows<T, 1, 1>(A, s);
+    else if (vecs <= 2 * 64 * kLpVecs)
+        launch_rows<T, 1, kLpVecs>(A, s);
     else
-        launch_lp<T, 8, 8>(A, s);
+        launch_rows<T, 4, kLpVecs>(A, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || A.splits == 1) return e;
-    hipLaunchKernelGGL((k_logprobs_join<T>), dim3((unsigned)std::min<int64_t>(A.n, kLpGrid)), dim3(kBlock),
-                       (size_t)A.splits * A.top * 8, s, A);
+    if (A.top > 0)
+        hipLaunchKernelGGL((k_logprobs_join<T, true>), dim3((unsigned)std::min<int64_t>(A.n, kLpGrid)), dim3(kBlock),
+                           (size_t)A.splits * A.top * 16, s, A);
+    else
+        hipLaunchKernelGGL((k_logprobs_join<T, false>), dim3((unsigned)std::min<int64_t>((A.n + 3) / 4, kLpGrid)),
+                           dim3(kBlock), 0, s, A);
     return hipGetLastError();
 }
 
@@ -586,7 +714,8 @@ int sk_scores_logprobs(const void* scores, int32_t dtype, int64_t n, int64_t m, 
     A.top_logp = top_logp;
     A.stats = stats;
     A.top_idx = top_idx;
-    A.splits = (int)L.splits;
+    A.splits = (int)L.cut.splits;
+    A.cut = L.cut.cut;
     A.pm = reinterpret_cast<float*>(base + L.pm);
     A.ps = reinterpret_cast<float*>(base + L.ps);
     A.px = reinterpret_cast<float*>(base + L.px);

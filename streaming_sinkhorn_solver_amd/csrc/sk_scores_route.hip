@@ -444,7 +444,8 @@ __global__ __launch_bounds__(kBlock) void k_route_finish(RouteArgs A) {
         if (tid == 0) have = 0;
         __syncthreads();
         for (int w = 0; w < kWaves; ++w) top = max(top, lane_top[w][lane]);
-        top = max(kth_of_wave(top, A.k), 1u);
+        const uint32_t lane_best[1] = {top};
+        top = max(kth_of_wave<0>(lane_best, A.k), 1u);
         for (int j = tid; j < A.m; j += kBlock)
             if ((uint32_t)(key[j] >> 32) >= top) list[atomicAdd(&have, 1)] = (uint16_t)j;
         __syncthreads();
