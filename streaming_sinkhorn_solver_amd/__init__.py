@@ -596,14 +596,25 @@ def _vec(t, n, dtype, device, name):
     return t.contiguous()
 
 
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, shape, dtype, device, name: str) -> torch.Tensor:
+    """_buf, without its checks where there is nothing to check (a call on a few rows is bound by the host)."""
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _buf(t, shape, dtype, device, name)
+
+
 def _call(name: str, device, *args):
     """Calls an entry point on the scores' device and its current stream (the last argument)."""
-    fn = getattr(load_library(), name)
+    fn = getattr(_lib or load_library(), name)
+    # the handle alone: a Stream object for it costs as much host time as a third of a small call
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
-        code = fn(*args, _stream(device))
+        code = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            code = fn(*args, _stream(device))
+            code = fn(*args, stream)
     if code:
         _raise(code, name)
 
@@ -634,10 +645,10 @@ def scores_solve(scores, a=None, b=None, *, eps: float, n_iters: int, g_init: to
             check_inputs(aa[:, None], bb[:, None], aa, bb)
     g_init = _vec(g_init, m, torch.float32, s.device, "g_init")
     ws = _ws(ws, s.device, lambda: scores_solve_workspace(n, m, s.device))
-    f = _buf(f, (n,), torch.float32, s.device, "f")
-    g = _buf(g, (m,), torch.float32, s.device, "g")
-    _call("sk_scores_solve", s.device, s.data_ptr(), code, n, m, ld, _ptr(a), _ptr(b), float(eps), int(n_iters),
-          _ptr(g_init), _ptr(f), _ptr(g), _ptr(ws), ws.numel())
+    f = _out(f, (n,), torch.float32, s.device, "f")
+    g = _out(g, (m,), torch.float32, s.device, "g")
+    _call("sk_scores_solve", s.device, s.data_ptr(), code, n, m, ld, _addr(a), _addr(b), float(eps), int(n_iters),
+          _addr(g_init), _addr(f), _addr(g), _addr(ws), ws.numel())
     return f, g
 
 
@@ -665,12 +676,13 @@ def scores_route(scores, k: int, *, score_fn: str = "softmax", bias: torch.Tenso
     if not 1 <= k <= m:
         raise ValueError(f"k must be between 1 and the {m} columns (got {k})")
     bias = _vec(bias, m, torch.float32, s.device, "bias")
-    idx = _buf(out.idx if out else None, (n, k), torch.int32, s.device, "out.idx")
-    weights = _buf(out.weights if out else None, (n, k), torch.float32, s.device, "out.weights")
-    cnt = _buf(out.counts if out else None, (m,), torch.int32, s.device, "out.counts") if counts else None
-    _call("sk_scores_route", s.device, s.data_ptr(), code, n, m, ld, SCORE_FNS[score_fn], _ptr(bias),
+    o_idx, o_weights, o_counts = out or (None, None, None)
+    idx = _out(o_idx, (n, k), torch.int32, s.device, "out.idx")
+    weights = _out(o_weights, (n, k), torch.float32, s.device, "out.weights")
+    cnt = _out(o_counts, (m,), torch.int32, s.device, "out.counts") if counts else None
+    _call("sk_scores_route", s.device, s.data_ptr(), code, n, m, ld, SCORE_FNS[score_fn], _addr(bias),
           SELECT_ON[select_on], int(n_group), int(topk_group), int(group_top), k, int(bool(renorm)), float(scale),
-          idx.data_ptr(), weights.data_ptr(), _ptr(cnt))
+          idx.data_ptr(), weights.data_ptr(), _addr(cnt))
     return Routing(idx, weights, cnt)
 
 
@@ -724,14 +736,16 @@ def scores_logprobs(scores, targets: torch.Tensor | None = None, *, eps: float =
     dev = s.device
     targets = _vec(targets, n, torch.int64, dev, "targets")
     ws = _ws(ws, dev, lambda: scores_logprobs_workspace(s.dtype, n, m, top, dev))
-    logp = None if targets is None else _buf(out.logp if out else None, (n,), torch.float32, dev, "out.logp")
-    lse = _buf(out.lse if out else None, (n,), torch.float32, dev, "out.lse")
-    ent = _buf(out.entropy if out else None, (n,), torch.float32, dev, "out.entropy") if entropy else None
-    top_idx = _buf(out.top_idx if out else None, (n, top), torch.int32, dev, "out.top_idx") if top > 0 else None
-    top_logp = _buf(out.top_logp if out else None, (n, top), torch.float32, dev, "out.top_logp") if top > 0 else None
-    stats = _buf(out.stats if out else None, (n, 2), torch.float32, dev, "out.stats")
-    _call("sk_scores_logprobs", dev, s.data_ptr(), code, n, m, ld, float(eps), _ptr(targets), top, _ptr(logp),
-          lse.data_ptr(), _ptr(ent), _ptr(top_idx), _ptr(top_logp), stats.data_ptr(), ws.data_ptr(), ws.numel())
+    o_logp, o_lse, o_ent, o_idx, o_top, o_stats = out or (None,) * 6
+    f32 = torch.float32
+    logp = None if targets is None else _out(o_logp, (n,), f32, dev, "out.logp")
+    lse = _out(o_lse, (n,), f32, dev, "out.lse")
+    ent = _out(o_ent, (n,), f32, dev, "out.entropy") if entropy else None
+    top_idx = _out(o_idx, (n, top), torch.int32, dev, "out.top_idx") if top > 0 else None
+    top_logp = _out(o_top, (n, top), f32, dev, "out.top_logp") if top > 0 else None
+    stats = _out(o_stats, (n, 2), f32, dev, "out.stats")
+    _call("sk_scores_logprobs", dev, s.data_ptr(), code, n, m, ld, float(eps), _addr(targets), top, _addr(logp),
+          lse.data_ptr(), _addr(ent), _addr(top_idx), _addr(top_logp), stats.data_ptr(), ws.data_ptr(), ws.numel())
     return Logprobs(logp, lse, ent, top_idx, top_logp, stats)
 
 
@@ -758,8 +772,8 @@ def scores_logprobs_grad(scores, targets: torch.Tensor | None, fwd: Logprobs, *,
     d_entropy = _vec(d_entropy, n, torch.float32, dev, "d_entropy")
     d_top = _vec(d_top, (n, top), torch.float32, dev, "d_top")
     grad = _grad_buf(grad, s)
-    _call("sk_scores_logprobs_grad", dev, s.data_ptr(), code, n, m, ld, float(eps), _ptr(targets), stats.data_ptr(),
-          _ptr(ent), top, _ptr(top_idx), _ptr(d_logp), _ptr(d_lse), _ptr(d_entropy), _ptr(d_top), grad.data_ptr(),
+    _call("sk_scores_logprobs_grad", dev, s.data_ptr(), code, n, m, ld, float(eps), _addr(targets), stats.data_ptr(),
+          _addr(ent), top, _addr(top_idx), _addr(d_logp), _addr(d_lse), _addr(d_entropy), _addr(d_top), grad.data_ptr(),
           max(grad.stride(0), m))
     return grad
 
