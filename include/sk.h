@@ -462,9 +462,10 @@ int sk_fs2_solve(const float *x, const float *y, const float *a, const float *b,
  *
  * A score of -inf is masked: it has probability zero.  A row that the mask
  * leaves empty gives the finite or infinite values stated with each entry
- * point, never NaN.  A NaN or +inf score makes the floating outputs of its row
- * NaN; indices stay valid and distinct, a NaN ranking as -inf.  Ties rank by
- * the lower index.  Results are deterministic.  All calls enqueue only
+ * point, never NaN.  A NaN or +inf score may make the floating outputs of its
+ * row NaN and, except in sk_scores_solve, of no other row; indices stay valid and
+ * distinct, a NaN ranking as -inf.  Ties rank by the lower index.  Results are
+ * deterministic.  All calls enqueue only
  * (capturable); a workspace may be shared by calls that are ordered in one stream,
  * not by graphs or streams that run at the same time.
  */
@@ -480,7 +481,7 @@ size_t sk_scores_solve_workspace_bytes(int64_t n, int64_t m);
  *     g_j <- -eps * LSE_i[(f_i + s_ij)/eps + log a_i].
  * a (n) and b (m) are weights of equal mass, used as given; NULL means uniform
  * 1/n, 1/m.  For a router, rows are tokens (weight 0 for padding, whose scores
- * are then not looked at) and columns experts (b their capacities); with b
+ * then reach nothing but their own f) and columns experts (b their capacities); with b
  * uniform, g is the bias under which the plan a_i b_j exp((f_i + g_j + s_ij)/eps)
  * loads the experts evenly: pass it to sk_scores_route with select_on = 1.
  * Each iteration reads the scores once and takes one exponential per score.

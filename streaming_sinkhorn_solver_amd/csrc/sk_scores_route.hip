@@ -10,7 +10,10 @@
 // One row per L lanes with E scores each, in registers.  Wide rows find the
 // (k + 1)-th largest of the lanes' maxima, a lower bound of the (k + 1)-th
 // largest value, and rank the few entries above it by counting; narrow rows, and
-// rows whose largest entries crowd into a few lanes, take k + 1 rounds of an argmax.
+// rows whose largest entries crowd into a few lanes, take k + 1 rounds of an argmax
+// (16384 x 256, k = 8: 30 us in rounds alone, 14 ranked; with k = 16 of 16 lanes,
+// where the bound is not used, 23).  The kernel is bound by latency and issue, not by the
+// 16.8 MB that it reads: about 600 vector instructions per wave of four rows.
 //
 // The order of two values that are closer than the float32 rounding of act or
 // of the sum with the bias would depend on that rounding.  The choice is
@@ -82,10 +85,12 @@ __device__ __forceinline__ R choice_value(const RouteArgs& A, float s, float bia
 //  sigmoid: the exponential's error (1.25 |s| + 1) enters by 1 - sigmoid, and
 //    |s| sigmoid (1 - sigmoid) < 0.28; sum and reciprocal add 1.5: less than 4 steps.
 //  the sum with the bias adds half a step of the value.
+// A masked score's act and an expert switched off by a bias of -inf are exact.
 constexpr float kStep = 0x1p-23f;
 __device__ __forceinline__ float choice_error(const RouteArgs& A, float s, float v, float M, float inv_S) {
+    if (v == -INFINITY) return 0.0f;
     float err = A.bias ? fabsf(v) * kStep : 0.0f;
-    if (!A.raw) err += A.sigmoid ? 4.0f * kStep * fminf(1.0f, 2.0f * exp_of(s)) : exp_of(s - M) * inv_S * (2.0f * (M - s) + 32.0f) * kStep;
+    if (!A.raw) err += A.sigmoid ? 4.0f * kStep * fminf(1.0f, 2.0f * exp_of(s)) : exp_of(s - M) * inv_S * (2.0f * fminf(M - s, 128.0f) + 32.0f) * kStep;
     return err;
 }
 // The most that act's part of it can be in the row (act (2 d + 32) falls with d).
@@ -287,8 +292,10 @@ __device__ __forceinline__ void store_weights(const RouteArgs& A, const uint16_t
     }
 }
 
+// Four waves per SIMD hide the latency of its short chains (16384 x 256: 14.3 us, 16.3 at the two that the
+// compiler's own choice of registers leaves); the widest rows need the registers of two.
 template <class T, int L, int E, bool V>
-__global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
+__global__ __launch_bounds__(kBlock, L * E <= 512 ? 4 : 2) void k_route(RouteArgs A) {
     constexpr int kSlots = kBlock / L;
     using Rw = Row<T, L, E, V>;
     using Elem = typename T::type;
@@ -356,7 +363,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
                 const int j0 = W.won[row][r], j1 = W.won[row][r + 1];
                 const float v0 = key_at(j0), v1 = key_at(j1);
                 // the first column left out stands for all others, whose act may be larger
-                const float e1 = r + 1 == A.k ? fabsf(v1) * kStep + act_err : choice_error(A, W.s[row][j1], v1, M, inv_S);
+                const float e1 = r + 1 == A.k && v1 > -INFINITY ? fabsf(v1) * kStep + act_err : choice_error(A, W.s[row][j1], v1, M, inv_S);
                 if (v0 - v1 <= choice_error(A, W.s[row][j0], v0, M, inv_S) + e1) close = true;
             }
         }

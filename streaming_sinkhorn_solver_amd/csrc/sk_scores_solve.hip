@@ -74,9 +74,24 @@ __device__ __forceinline__ float row_step(const SolveArgs& A, float (&t)[E], flo
 
 __device__ __forceinline__ float log2_b(const SolveArgs& A, int j) { return A.b ? s_lg2(A.b[j]) : -s_lg2((float)A.m); }
 
-// Whether the sum c_j is sure to hold what its n terms add up to: each loses at
-// most 2^-126 to the exponential's flush, so above n 2^-100 less than a rounding is lost.
-__device__ __forceinline__ bool safe(const SolveArgs& A, float cj) { return cj >= (float)A.n * 0x1p-100f; }
+// Whether the sum c_j is sure to hold what its n terms a_i q_ij add up to: a term loses at most a_i 2^-126 to the
+// exponential's flush and 2^-126 to its own, so above (mass + n) 2^-100 less than a rounding is lost.
+__device__ __forceinline__ bool safe(const SolveArgs& A, float cj, float mass) { return cj >= (mass + (float)A.n) * 0x1p-100f; }
+
+// The mass of the weights, by the whole workgroup (through its columns' side, which is the shorter one).
+template <int THREADS>
+__device__ float total_mass(const SolveArgs& A) {
+    if (!A.b) return 1.0f;
+    __shared__ float part[THREADS / 64];
+    float sum = 0.0f;
+    for (int j = threadIdx.x; j < A.m; j += THREADS) sum += A.b[j];
+    sum = lanes_sum<64>(sum);
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int w = 0; w < THREADS / 64; ++w) sum += part[w];
+    return sum;
+}
 
 // The column half-step of one column by its log-sum-exp over the rows, by the whole workgroup.
 template <class T, int THREADS>
@@ -179,6 +194,7 @@ __global__ __launch_bounds__(kBlock) void k_solve_update(SolveArgs A) {
         }
     }
     sum[y][x] = part;
+    const float mass = total_mass<kBlock>(A);
     __syncthreads();
     if (y == 0) {
         float cj = 0.0f;
@@ -186,7 +202,7 @@ __global__ __launch_bounds__(kBlock) void k_solve_update(SolveArgs A) {
         for (int k = 0; k < kSlices; ++k) cj += sum[k][x];
         int need = 0;
         if (j < A.m) {
-            if (lb > -INFINITY && safe(A, cj))
+            if (lb > -INFINITY && safe(A, cj, mass))
                 A.g[j] = fmaf(A.inv_c, lb - s_lg2(cj), g);
             else if (lb == -INFINITY && !A.last)
                 A.g[j] = g;  // a column of weight zero enters no row before the last iteration
@@ -233,6 +249,7 @@ __global__ __launch_bounds__(kSolveThreads) void k_solve_small(SolveArgs A) {
 #pragma unroll
     for (int e = 0; e < E; ++e) lb[e] = red[0][Rw::col(e, l)];
     if (threadIdx.x < 2) direct[threadIdx.x] = 0;
+    const float mass = total_mass<kSolveThreads>(A);
     for (int k = 0; k < A.iters; ++k) {
         __syncthreads();
         float h[E], acc[E];
@@ -269,7 +286,7 @@ __global__ __launch_bounds__(kSolveThreads) void k_solve_small(SolveArgs A) {
             float cj = 0.0f;
 #pragma unroll
             for (int q = 0; q < kWaves; ++q) cj += red[q][j];
-            if (b2 > -INFINITY && safe(A, cj))
+            if (b2 > -INFINITY && safe(A, cj, mass))
                 g[j] = fmaf(A.inv_c, b2 - s_lg2(cj), g[j]);
             else
                 need = b2 > -INFINITY || last;

@@ -129,6 +129,27 @@ def test_masks_and_extremes(dtype, renorm, fn):
     check(x, s, 6, dtype, score_fn=fn, renorm=renorm, bias=bias, select_on="logit")
 
 
+@pytest.mark.parametrize("fn", ["softmax", "sigmoid"])
+def test_masks_with_a_bias(fn):
+    """Masked experts decided by their bias alone, next to values that were rounded; exactly k experts left on."""
+    r = np.random.default_rng(5)
+    n, m, k = 300, 48, 6
+    x, s = matrix(n, m, "f32", 17, spread=1.0, mask=0.7)
+    bias = (r.integers(0, 3, m) * np.float32(0.25)).astype(np.float32)
+    check(x, s, k, "f32", score_fn=fn, bias=bias)
+    # an unmasked expert whose value equals a masked one's up to the last bits
+    act = osc.route_values(s, fn, None, "score")
+    for i in range(n):
+        j = int(np.argmax(np.where(np.isfinite(s[i]), s[i], -np.inf)))
+        bias[j % m] = np.float32(0.5 - act[i, j])
+    check(x, s, k, "f32", score_fn=fn, bias=bias)
+    off = np.full(m, -np.inf, np.float32)
+    off[r.permutation(m)[:k]] = r.normal(size=k)
+    check(x, s, k, "f32", score_fn=fn, bias=off)
+    check(x, s, k, "f32", score_fn=fn, bias=off, select_on="logit")
+    check(x, s, k, "f32", score_fn=fn, bias=off, n_group=4, topk_group=2, group_top=2)
+
+
 def test_nan_and_infinity_leave_valid_choices():
     x, _ = matrix(64, 100, "f32", 9)
     x[3, 5] = float("nan")

@@ -81,6 +81,18 @@ def test_zero_weights_masks_and_far_columns(n, m):
             assert g[2] > 200
 
 
+@pytest.mark.parametrize("n", [200, 5000])
+@pytest.mark.parametrize("mass", [1.0, 2.0 ** 66])
+def test_far_column_at_any_mass(n, mass):
+    """A column whose shares lie around the smallest float32 exponential: one row's share is kept, the others' are flushed."""
+    s = np.zeros((n, 3), np.float32)
+    s[:, 1] = -87.6
+    s[3, 1] = -86.0
+    a, b = np.full(n, mass / n, np.float32), np.array([mass / 2, mass / 4, mass / 4], np.float32)
+    for iters in (1, 3):
+        check(torch.from_numpy(s).to(DEV), s.astype(np.float64), a, b, 1.0, iters)
+
+
 def test_equals_the_point_cloud_solver():
     """The same costs through the library's own solver: C = |x - y|^2 as scores -C."""
     x, y, a, b = random_problem(300, 200, 3, 5)
