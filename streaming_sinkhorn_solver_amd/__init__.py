@@ -12,6 +12,10 @@ otherwise), zeros legal -- all on the same CUDA/HIP device.  float64 inputs
 raise ValueError: the kernels are float32-only.  The cost is
 C_ij = |x_i - y_j|^2 with no 1/2 factor; eps is measured against it.
 Potentials are returned in cost units (f, g), not divided by eps.
+
+The scores_* functions take a score matrix instead of clouds, (n, m) float32,
+bfloat16 or float16 with any row stride: balancing potentials and routing of a
+router's scores, log-probabilities of a head's, and their gradients.
 """
 from __future__ import annotations
 

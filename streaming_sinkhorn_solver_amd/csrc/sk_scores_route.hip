@@ -293,9 +293,9 @@ __device__ __forceinline__ void store_weights(const RouteArgs& A, const uint16_t
 }
 
 // Four waves per SIMD hide the latency of its short chains (16384 x 256: 14.3 us, 16.3 at the two that the
-// compiler's own choice of registers leaves); the widest rows need the registers of two.
+// compiler's own choice of registers leaves; 8192 x 1024: 20.3 and 23.4).
 template <class T, int L, int E, bool V>
-__global__ __launch_bounds__(kBlock, L * E <= 512 ? 4 : 2) void k_route(RouteArgs A) {
+__global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
     constexpr int kSlots = kBlock / L;
     using Rw = Row<T, L, E, V>;
     using Elem = typename T::type;
