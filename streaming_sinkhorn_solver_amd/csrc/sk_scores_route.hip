@@ -7,22 +7,26 @@
 // the sum of its group_top largest v); ties go to the lowest index.  The
 // weights come from act at the chosen experts, without the bias.
 //
-// One row per L lanes with E scores each, in registers.  Wide rows find the
-// (k + 1)-th largest of the lanes' maxima, a lower bound of the (k + 1)-th
-// largest value, and rank the few entries above it by counting; narrow rows, and
-// rows whose largest entries crowd into a few lanes, take k + 1 rounds of an argmax
-// (16384 x 256, k = 8: 30 us in rounds alone, 14 ranked; with k = 16 of 16 lanes,
-// where the bound is not used, 23).  The kernel is bound by latency and issue, not by the
-// 16.8 MB that it reads: about 600 vector instructions per wave of four rows.
+// One row per L lanes with E scores each, in registers.  Wide rows find the k-th
+// largest of the lanes' maxima, a lower bound of the k-th largest value, and rank
+// the few entries above it by counting; narrow rows, and rows whose largest entries
+// crowd into a few lanes, take k rounds of an argmax (16384 x 256, k = 8: 30 us in
+// rounds alone, 14 ranked; with k = 16 of 16 lanes, where the bound is not used, 23).
+// The kernel is bound by latency and issue, not by the 16.8 MB that it reads: about
+// 600 vector instructions per wave of four rows.
 //
 // The order of two values that are closer than the float32 rounding of act or
 // of the sum with the bias would depend on that rounding.  The choice is
-// therefore checked against error bounds, which is what the (k + 1)-th is for, and
-// rows where a pair that decides is too close are marked (their first index is
-// stored as its complement); a second kernel, which also counts the rows per
-// expert, chooses those again in float64, a workgroup each: the result is that of the
-// definition.  (With the float64 code in the first kernel its registers leave two
-// waves per SIMD, or spill, and one doubtful row holds up the end of the launch.)
+// therefore checked against error bounds (one entry more than k is ranked for it),
+// and rows where a pair that decides is too close are marked: their first index is
+// stored as its complement.  Entries of equal score and equal bias tie exactly and
+// are not in doubt (16384 x 256 bf16 scores under a bias of zeros: 18 us; 186 with
+// their ties taken as doubt).  A second kernel, which also counts the rows per
+// expert, chooses the marked rows again in float64, a workgroup each: the result is
+// that of the definition.  (With the float64 code in the first kernel its registers
+// leave two waves per SIMD, or spill, and one doubtful row holds up the end of the
+// launch.)  Groups whose sums tie are in doubt: 16384 x 256 equal scores in 8 groups
+// send every row there and take 1.0 ms.
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -292,8 +296,8 @@ __device__ __forceinline__ void store_weights(const RouteArgs& A, const uint16_t
     }
 }
 
-// Four waves per SIMD hide the latency of its short chains (16384 x 256: 14.3 us, 16.3 at the two that the
-// compiler's own choice of registers leaves; 8192 x 1024: 20.3 and 23.4).
+// Four waves per SIMD hide the latency of its short chains (16384 x 256: 13.9 us, 16.3 at the two that the
+// compiler's own choice of registers leaves; 8192 x 1024: 20.1 and 23.4).
 template <class T, int L, int E, bool V>
 __global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
     constexpr int kSlots = kBlock / L;
@@ -315,7 +319,9 @@ __global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
     for (int j = threadIdx.x; j < L * E; j += kBlock) bias[j] = A.bias && j < A.m ? A.bias[j] : 0.0f;
     __syncthreads();
     const int left = A.n_group > 1 ? A.topk_group * A.group_size : A.m;
-    const int rounds = left > A.k ? A.k + 1 : A.k;
+    // where values are rounded, one more than k shows whether the last one chosen is apart from the first left out
+    const bool check = A.doubt && A.bias;
+    const int rounds = check ? min(left, A.k + 1) : A.k;
     for (int64_t i0 = (int64_t)blockIdx.x * kSlots; i0 < A.n; i0 += (int64_t)gridDim.x * kSlots) {
         const int64_t i = i0 + threadIdx.x / L;
         const bool on = i < A.n;
@@ -358,13 +364,32 @@ __global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
         for (int e = 0; e < E; ++e) W.s[row][Rw::col(e, l)] = s[e];
         wave_sync();
         choose<Rw, L, E>(W, key, l, row, rounds, key_at);
-        if (A.doubt && A.bias) {  // neighbours in the order must be apart
-            for (int r = l; r + 1 < rounds; r += L) {
+        if (check) {  // neighbours in the order must be apart, or equal in score and bias: then the column decides
+            auto tie = [&](int p, int q) { return W.s[row][p] == W.s[row][q] && bias[p] == bias[q]; };
+            auto error = [&](int j, float v) { return choice_error(A, W.s[row][j], v, M, inv_S); };
+            for (int r = l; r + 1 < A.k; r += L) {
                 const int j0 = W.won[row][r], j1 = W.won[row][r + 1];
                 const float v0 = key_at(j0), v1 = key_at(j1);
-                // the first column left out stands for all others, whose act may be larger
-                const float e1 = r + 1 == A.k && v1 > -INFINITY ? fabsf(v1) * kStep + act_err : choice_error(A, W.s[row][j1], v1, M, inv_S);
-                if (v0 - v1 <= choice_error(A, W.s[row][j0], v0, M, inv_S) + e1) close = true;
+                if (v0 - v1 <= error(j0, v0) + error(j1, v1) && !tie(j0, j1)) close = true;
+            }
+            if (rounds > A.k) {
+                // the first column left out stands for all others, whose act may be larger; where it ties with the last
+                // one chosen, the largest that does not
+                const int j0 = W.won[row][A.k - 1], j1 = W.won[row][A.k];
+                const float v0 = key_at(j0);
+                float below = key_at(j1);
+                const bool tied = tie(j0, j1);
+                if (__any(tied)) {
+                    float other = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int j = Rw::col(e, l);
+                        if (j < A.m && key[e] <= v0 && !tie(j0, j)) other = fmaxf(other, key[e]);
+                    }
+                    other = lanes_max<L>(other);
+                    below = tied ? other : below;
+                }
+                if (v0 - below <= error(j0, v0) + (below > -INFINITY ? fabsf(below) * kStep + act_err : 0.0f)) close = true;
             }
         }
         const bool marked = lanes_max<L>(close ? 1u : 0u) != 0;
@@ -461,10 +486,11 @@ __global__ __launch_bounds__(kBlock) void k_route_finish(RouteArgs A) {
             const int j = list[c];
             const uint64_t mine = key[j];
             int rank = 0;
+#pragma unroll 8
             for (int q = 0; q < count; ++q) {
                 const int jq = list[q];
                 const uint64_t x = key[jq];
-                rank += x > mine || (x == mine && jq < j) ? 1 : 0;
+                rank += (x > mine ? 1 : 0) + (((x == mine) & (jq < j)) ? 1 : 0);
             }
             if (rank < A.k) {
                 won[rank] = (uint16_t)j;

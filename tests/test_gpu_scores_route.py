@@ -104,6 +104,12 @@ def test_ties_and_close_values(m, fn):
     s = base.astype(np.float64)
     for how in (dict(), dict(bias=np.full(m, 0.25, np.float32)), dict(bias=np.full(m, 1000.0, np.float32), select_on="logit")):
         check(x, s, k, "f32", score_fn=fn, **how)
+    # 16-bit scores, most of them equal to another, under a bias that is equal too or is not
+    x, s = matrix(200, m, "bf16", m + 1, spread=1.0)
+    check(x, s, k, "bf16", score_fn=fn, bias=np.zeros(m, np.float32))
+    check(x, s, k, "bf16", score_fn=fn, bias=(r.integers(0, 2, m) * np.float32(2.0 ** -20)).astype(np.float32))
+    x = torch.from_numpy(base).to(DEV)
+    s = base.astype(np.float64)
     if m % 4 == 0:
         k = min(k, m // 2)  # half of the groups take part
         check(x, s, k, "f32", score_fn=fn, n_group=4, topk_group=2, group_top=2)
@@ -208,6 +214,15 @@ def test_no_rows_and_many_rows():
     r = sk.scores_route(x, 2, counts=True)
     assert torch.equal(r.idx.long(), x.topk(2, dim=1).indices)
     assert torch.equal(r.counts.long(), torch.bincount(r.idx.long().reshape(-1), minlength=12))
+
+
+@pytest.mark.parametrize("n,m,how", [(40_000, 64, dict(score_fn="sigmoid")),
+                                     (17_001, 48, dict(score_fn="softmax", n_group=4, topk_group=2, group_top=2))])
+def test_many_rows_in_doubt(n, m, how):
+    """More rows than the second kernel's workgroups take at once, many of them with values a bit apart."""
+    r = np.random.default_rng(n)
+    base = (r.integers(-2, 3, (n, m)) + r.integers(0, 4, (n, m)) * 2.0 ** -22).astype(np.float32)
+    check(torch.from_numpy(base).to(DEV), base.astype(np.float64), 6, "f32", bias=np.full(m, 0.125, np.float32), **how)
 
 
 def test_refusals():
