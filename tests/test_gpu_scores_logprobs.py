@@ -138,6 +138,45 @@ def test_top_orders(m, dtype, kind):
     check_forward(r, osc.logprobs(s, None, 1.0, top), s, None, 1.0, top)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,lanes", [(1500, 20), (3000, 20), (9000, 40), (70001, 40)])
+def test_more_crowded_entries_than_the_list_holds(m, lanes, dtype):
+    """The largest entries all lie in the columns of a few threads, more of them than are kept: fewer classes than k."""
+    n, top = 3, 64
+    per = 8 if dtype == "bf16" else 4  # scores of 16 bytes
+    r = np.random.default_rng(m)
+    v = np.arange(m) // per % (64 if m <= 3000 else 256)
+    x = torch.from_numpy(np.where(v < lanes, 10.0 + r.normal(size=(n, m)), r.normal(size=(n, m))).astype(np.float32)).to(DEV)
+    x = x.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    s = x.double().cpu().numpy()
+    r = sk.scores_logprobs(x, top=top)
+    check_forward(r, osc.logprobs(s, None, 1.0, top), s, None, 1.0, top)
+
+
+@pytest.mark.parametrize("kind", ["equal", "two_values", "masked", "rounded"])
+def test_ties_in_whole_rows(kind):
+    """Enough rows that none is cut: more blocks reach the bound than the list of them holds."""
+    n, m, top = 1030, 17003, 20
+    x = torch.zeros((n, m), dtype=torch.bfloat16, device=DEV)
+    torch.manual_seed(3)
+    if kind == "two_values":
+        x[torch.rand((n, m), device=DEV) < 0.3] = 1.0
+    elif kind == "masked":
+        x[torch.rand((n, m), device=DEV) < 0.9995] = -float("inf")
+    elif kind == "rounded":
+        x.copy_(torch.randn((n, m), device=DEV).round())
+    r = sk.scores_logprobs(x, top=top)
+    order = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :top]
+    assert torch.equal(r.top_idx.long(), order)
+    want = torch.log_softmax(x.double(), 1)
+    lse = torch.logsumexp(x.double(), 1)
+    # 400 half steps (150 additions, the terms' own errors, the logarithm) of values below 16
+    assert (r.lse - lse).abs().max() < 400 * U * 16
+    got = want.gather(1, order)
+    fin = torch.isfinite(got)
+    assert torch.equal(torch.isfinite(r.top_logp), fin) and (r.top_logp - got)[fin].abs().max() < 400 * U * 16
+
+
 def test_nan_and_infinity_stay_in_their_rows():
     x, s = matrix(5, 5000, "f32", 1)
     x[1, 77] = float("nan")
@@ -174,7 +213,7 @@ def test_no_rows_and_many_rows():
     x = torch.randn((n, 5), device=DEV)
     t = torch.randint(0, 5, (n,), device=DEV)
     r = sk.scores_logprobs(x, t, top=2)
-    want = torch.log_softmax(x.double(), 1)
+    want = torch.log_softmax(x.double(), 1)  # 200 half steps of log-probabilities below 8, of gradients below 2
     assert (r.logp - want.gather(1, t[:, None])[:, 0]).abs().max() < 200 * U * 8
     assert torch.equal(r.top_idx[:, 0].long(), x.argmax(1))
     g = sk.scores_logprobs_grad(x, t, r, d_logp=torch.ones(n, device=DEV))
