@@ -86,15 +86,20 @@ __device__ __forceinline__ R choice_value(const RouteArgs& A, float s, float bia
 //  softmax: an exponent d carries less than 1.25 d steps, the hardware's exp2 one;
 //    the sum of at most 16 + 6 additions 11 steps and its terms' own mean error, at most
 //    1.25 log m + 1 < 10; reciprocal and product 2: less than act (2 d + 32) steps.
-//  sigmoid: the exponential's error (1.25 |s| + 1) enters by 1 - sigmoid, and
-//    |s| sigmoid (1 - sigmoid) < 0.28; sum and reciprocal add 1.5: less than 4 steps.
+//  sigmoid: the exponential's relative error, less than 1.25 |s| + 1 steps, enters by the factor 1 - sigmoid, where
+//    |s| (1 - sigmoid) < 0.28 for s > 0; sum and reciprocal add 1.5: less than act (4 + 1.25 max(0, -s)) steps.
+//    That is less than 4 steps, as s falls from 0 act falls faster than the factor rises.
 //  the sum with the bias adds half a step of the value.
-// A masked score's act and an expert switched off by a bias of -inf are exact.
-constexpr float kStep = 0x1p-23f;
+// An act below 2^-126 may be off by that much (subnormal, or flushed). A masked score's act and an expert switched off
+// by a bias of -inf are exact.
+constexpr float kStep = 0x1p-23f, kLost = 0x1p-126f;
 __device__ __forceinline__ float choice_error(const RouteArgs& A, float s, float v, float M, float inv_S) {
     if (v == -INFINITY) return 0.0f;
     float err = A.bias ? fabsf(v) * kStep : 0.0f;
-    if (!A.raw) err += A.sigmoid ? 4.0f * kStep * fminf(1.0f, 2.0f * exp_of(s)) : exp_of(s - M) * inv_S * (2.0f * fminf(M - s, 128.0f) + 32.0f) * kStep;
+    if (!A.raw) {
+        err += kLost + kStep * (A.sigmoid ? sigmoid_of(s) * (4.0f + 1.25f * fminf(fmaxf(0.0f, -s), 128.0f))
+                                          : exp_of(s - M) * inv_S * (2.0f * fminf(M - s, 128.0f) + 32.0f));
+    }
     return err;
 }
 // The most that act's part of it can be in the row (act (2 d + 32) falls with d).

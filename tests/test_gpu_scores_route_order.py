@@ -1,0 +1,61 @@
+"""The order of scores_route where float32 cannot tell values apart by itself: far negative sigmoid scores, values
+around the smallest normal number, sums beyond the largest."""
+import numpy as np
+import pytest
+import torch
+
+import streaming_sinkhorn_solver_amd as sk
+from oracle import scores as osc
+from scores_cases import DEV
+
+pytestmark = pytest.mark.gpu
+
+F = np.float32
+
+
+def logit(p):
+    return (np.log(p) - np.log1p(-p)).astype(F)
+
+
+def same_choice(s, k, dtype=torch.float32, **how):
+    """idx and counts are those of the float64 reference."""
+    x = torch.from_numpy(s).to(dtype)
+    d = dict(how)
+    bias = d.pop("bias", None)
+    r = sk.scores_route(x.to(DEV), k, bias=None if bias is None else torch.from_numpy(bias).to(DEV), counts=True, **d)
+    idx, _, cnt = osc.route(x.double().numpy(), k, fn=d.pop("score_fn", "softmax"), bias=bias, **d)
+    wrong = (r.idx.cpu().numpy() != idx).any(1)
+    assert not wrong.any(), f"{wrong.sum()} of {len(wrong)} rows, the first {np.flatnonzero(wrong)[0]}"
+    assert np.array_equal(r.counts.cpu().numpy(), cnt)
+
+
+@pytest.mark.parametrize("low", [-5, -12, -23, -40, -60, -80, -87, -95])
+@pytest.mark.parametrize("m", [2, 40, 300])
+def test_far_negative_sigmoid_scores_under_a_bias_of_their_size(m, low):
+    """Two columns whose act and bias add up to almost the same number, the others far below them: the relative error of
+    a float32 sigmoid grows with the score."""
+    r = np.random.default_rng(m - low)
+    a = np.exp(low)
+    b = (-a * np.array([0.3, 0.9])).astype(F)
+    act = a * (1 + r.random((20000, 1))) - b
+    s = np.full((20000, m), -np.inf, F)
+    bias = np.full(m, -1.0, F)
+    s[:, [0, m - 1]], bias[[0, m - 1]] = logit(act), b
+    same_choice(s, 2, score_fn="sigmoid", bias=bias)
+
+
+def test_two_far_negative_sigmoid_scores():
+    """Float32 values 3.0e-16 apart, in the other order than the values themselves."""
+    s = np.array([[-22.945890426635742, -22.961633682250977]], F)
+    same_choice(s, 2, score_fn="sigmoid", bias=np.array([-9.749198670583326e-11, -9.579995824404719e-11], F))
+
+
+@pytest.mark.parametrize("low", [-30, -87, -95])
+def test_far_softmax_acts_under_a_bias_of_their_size(low):
+    """The same for softmax, whose bound grows with the distance to the row's maximum; subnormal acts among them."""
+    r = np.random.default_rng(-low)
+    a = np.exp(low)
+    b = (-a * np.array([0.0, 0.3, 0.9])).astype(F)
+    s = np.log(a * (1 + r.random((20000, 1))) - b.astype(np.float64)).astype(F)
+    s[:, 0] = 0.0
+    same_choice(s, 3, score_fn="softmax", bias=b)
