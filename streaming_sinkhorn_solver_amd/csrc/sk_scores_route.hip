@@ -179,9 +179,13 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& A, RouteWave<L, E>&
         const float sum = key_of(v1 + v2);
         float err = fabsf(sum) * kStep;
         if (A.bias) err += (fabsf(v1) + fabsf(v2)) * kStep + 2.0f * act_err;
-        // without a bias v is act itself: 4 steps of it, or 2 d + 32 with d = log(1 / (act S))
-        if (!A.bias && !A.raw)
-            err += (v1 + v2) * kStep * (A.sigmoid ? 4.0f : 32.0f + 2.0f * kLn2 * fmaxf(0.0f, s_lg2(inv_S) - s_lg2(fmaxf(v2, 0x1p-126f))));
+        // without a bias v is act itself, and both are off by no more than the smaller one's factor: 2 d + 32 steps with
+        // d = log(1 / (act S)), or 4 + 1.25 max(0, -s) with -s <= log(1 / act)
+        if (!A.bias && !A.raw) {
+            const float far = -s_lg2(fmaxf(v2, 0x1p-126f));  // log2(1 / act)
+            const float steps = A.sigmoid ? 4.0f + 1.25f * kLn2 * far : 32.0f + 2.0f * kLn2 * fmaxf(0.0f, s_lg2(inv_S) + far);
+            err += (v1 + v2) * kStep * steps;
+        }
         if (g < A.n_group) {
             if (sum > -INFINITY) worst_err = fmaxf(worst_err, err);  // (a masked group's score is exact)
             if (sub == 0) W.gscore[row][g] = sum;

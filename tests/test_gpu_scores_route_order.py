@@ -59,3 +59,17 @@ def test_far_softmax_acts_under_a_bias_of_their_size(low):
     s = np.log(a * (1 + r.random((20000, 1))) - b.astype(np.float64)).astype(F)
     s[:, 0] = 0.0
     same_choice(s, 3, score_fn="softmax", bias=b)
+
+
+@pytest.mark.parametrize("lo,hi", [(-5, -2), (-16, -12), (-30, -25), (-60, -55), (-86, -84)])
+@pytest.mark.parametrize("size", [2, 20])
+def test_groups_of_far_negative_sigmoid_scores(size, lo, hi):
+    """Two groups whose two largest values add up to almost the same sum."""
+    r = np.random.default_rng(size - lo)
+    x = r.uniform(lo, hi, (60000, 3)).astype(F)
+    p = osc._sigmoid(x.astype(np.float64))
+    rest = p[:, 0] + p[:, 1] - p[:, 2]
+    x, rest = x[rest > np.exp(lo - 1.0)], rest[rest > np.exp(lo - 1.0)]
+    s = np.full((len(x), 2 * size), -np.inf, F)
+    s[:, 0], s[:, size - 1], s[:, size], s[:, -1] = x[:, 0], x[:, 1], x[:, 2], logit(rest)
+    same_choice(s, 2, score_fn="sigmoid", n_group=2, topk_group=1, group_top=2)
