@@ -180,11 +180,11 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& A, RouteWave<L, E>&
         float err = fabsf(sum) * kStep;
         if (A.bias) err += (fabsf(v1) + fabsf(v2)) * kStep + 2.0f * act_err;
         // without a bias v is act itself, and both are off by no more than the smaller one's factor: 2 d + 32 steps with
-        // d = log(1 / (act S)), or 4 + 1.25 max(0, -s) with -s <= log(1 / act)
+        // d = log(1 / (act S)), or 4 + 1.25 max(0, -s) with -s <= log(1 / act); each may have lost kLost
         if (!A.bias && !A.raw) {
             const float far = -s_lg2(fmaxf(v2, 0x1p-126f));  // log2(1 / act)
             const float steps = A.sigmoid ? 4.0f + 1.25f * kLn2 * far : 32.0f + 2.0f * kLn2 * fmaxf(0.0f, s_lg2(inv_S) + far);
-            err += (v1 + v2) * kStep * steps;
+            err += (v1 + v2) * kStep * steps + 2.0f * kLost;
         }
         if (g < A.n_group) {
             if (sum > -INFINITY) worst_err = fmaxf(worst_err, err);  // (a masked group's score is exact)

@@ -73,3 +73,14 @@ def test_groups_of_far_negative_sigmoid_scores(size, lo, hi):
     s = np.full((len(x), 2 * size), -np.inf, F)
     s[:, 0], s[:, size - 1], s[:, size], s[:, -1] = x[:, 0], x[:, 1], x[:, 2], logit(rest)
     same_choice(s, 2, score_fn="sigmoid", n_group=2, topk_group=1, group_top=2)
+
+
+@pytest.mark.parametrize("lo,hi", [(-88.2, -86.8), (-88.7, -87.4), (-89.5, -88.5), (-103.0, -99.0)])
+@pytest.mark.parametrize("size", [2, 20])
+def test_groups_of_sigmoids_below_the_smallest_normal_number(size, lo, hi):
+    """Group sums of subnormal sigmoids, and of some whose exponential is infinite in float32."""
+    r = np.random.default_rng(size)
+    n, groups = 20000, 4
+    s = np.full((n, groups, size), -np.inf, F)
+    s[:, :, :2] = r.uniform(lo, hi, (n, groups, 2))
+    same_choice(s.reshape(n, -1), 3, score_fn="sigmoid", n_group=groups, topk_group=2, group_top=2)
