@@ -175,16 +175,17 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& A, RouteWave<L, E>&
             k2 = fmaxf(fminf(k1, y1), fmaxf(k2, y2));
             k1 = fmaxf(k1, y1);
         }
-        const float v1 = k1, v2 = A.group_top == 2 ? k2 : 0.0f;
+        // (half the sum of two values, which does not overflow, and is exact but for subnormal ones)
+        const float v1 = A.group_top == 2 ? 0.5f * k1 : k1, v2 = A.group_top == 2 ? 0.5f * k2 : 0.0f;
         const float sum = key_of(v1 + v2);
-        float err = fabsf(sum) * kStep;
+        float err = fabsf(sum) * kStep + kLost;
         if (A.bias) err += (fabsf(v1) + fabsf(v2)) * kStep + 2.0f * act_err;
         // without a bias v is act itself, and both are off by no more than the smaller one's factor: 2 d + 32 steps with
         // d = log(1 / (act S)), or 4 + 1.25 max(0, -s) with -s <= log(1 / act); each may have lost kLost
         if (!A.bias && !A.raw) {
-            const float far = -s_lg2(fmaxf(v2, 0x1p-126f));  // log2(1 / act)
+            const float far = -s_lg2(fmaxf(k2, 0x1p-126f));  // log2(1 / act)
             const float steps = A.sigmoid ? 4.0f + 1.25f * kLn2 * far : 32.0f + 2.0f * kLn2 * fmaxf(0.0f, s_lg2(inv_S) + far);
-            err += (v1 + v2) * kStep * steps + 2.0f * kLost;
+            err += (v1 + v2) * kStep * steps + kLost;
         }
         if (g < A.n_group) {
             if (sum > -INFINITY) worst_err = fmaxf(worst_err, err);  // (a masked group's score is exact)

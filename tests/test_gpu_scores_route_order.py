@@ -84,3 +84,21 @@ def test_groups_of_sigmoids_below_the_smallest_normal_number(size, lo, hi):
     s = np.full((n, groups, size), -np.inf, F)
     s[:, :, :2] = r.uniform(lo, hi, (n, groups, 2))
     same_choice(s.reshape(n, -1), 3, score_fn="sigmoid", n_group=groups, topk_group=2, group_top=2)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [2, 16])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_group_sums_beyond_float32(with_bias, size, dtype):
+    """Masks of -inf and of the type's lowest value side by side, and groups of numbers near the largest."""
+    r = np.random.default_rng(size)
+    n, groups = 500, 8
+    big = torch.finfo(dtype).max
+    s = r.choice(np.array([-np.inf, -big], F), (n, groups, size))
+    dead = r.random((n, groups)) < 0.5
+    s[dead] = -np.inf
+    s[: n // 2, :, 0] = np.where(r.random((n // 2, groups)) < 0.2, F(1.0), s[: n // 2, :, 0])
+    s[-100:] = big * r.choice(np.array([0.5, 0.625, 0.75, 0.875, 1.0]), (100, groups, size))
+    bias = np.zeros(groups * size, F) if with_bias else None
+    for topg in (1, 3):
+        same_choice(s.reshape(n, -1).astype(F), 2, dtype, select_on="logit", bias=bias, n_group=groups, topk_group=topg, group_top=2)
