@@ -102,3 +102,17 @@ def test_group_sums_beyond_float32(with_bias, size, dtype):
     bias = np.zeros(groups * size, F) if with_bias else None
     for topg in (1, 3):
         same_choice(s.reshape(n, -1).astype(F), 2, dtype, select_on="logit", bias=bias, n_group=groups, topk_group=topg, group_top=2)
+
+
+@pytest.mark.parametrize("m,k", [(8, 8), (8, 3), (40, 12), (300, 20)])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_score_and_bias_beyond_float32(sign, m, k):
+    """Scores and biases near the type's ends: their sum is finite, whatever float32 makes of it."""
+    r = np.random.default_rng(m)
+    big = np.finfo(F).max
+    s = r.choice(np.array([-np.inf if sign < 0 else 1.0, sign * big, sign * 0.75 * big, 0.5], F), (400, m), p=[0.4, 0.3, 0.25, 0.05])
+    bias = (sign * r.choice(np.array([0.0, 0.5, 0.75, 1.0]), m) * big).astype(F)
+    same_choice(s, k, select_on="logit", bias=bias)
+    if m % 4 == 0 and k <= m // 2:
+        for gt in (1, 2):
+            same_choice(s, k, select_on="logit", bias=bias, n_group=4, topk_group=2, group_top=gt)
