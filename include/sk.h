@@ -501,9 +501,12 @@ int sk_scores_solve(const void *scores, int32_t dtype, int64_t n, int64_t m, int
  * floats or NULL).  With n_group > 1 (a divisor of m, <= 64) only the topk_group
  * best groups of m / n_group neighbouring columns take part, a group's score
  * being the sum of its group_top (1 or 2) largest v.  idx (n, k) receives the
- * k <= 64 largest v in descending order, ties by the lower index; the order
- * is that of the definition (values closer than float32 can tell apart are
- * taken in float64).  weights (n, k) are act at idx, without the bias, divided by
+ * k <= 64 largest v in descending order, ties by the lower index.  The order is
+ * that of v in float64 (values that float32 cannot tell apart are taken in float64),
+ * so columns whose act + bias rounds to one float64 number tie.  Without a bias act
+ * keeps the scores' order and the scores themselves decide (inside the chosen groups
+ * too), also where act saturates: no bias and a bias of zeros may then choose
+ * differently.  weights (n, k) are act at idx, without the bias, divided by
  * their sum with renorm = 1 (exact also where act underflows), times scale; a
  * chosen expert that is masked has weight 0.  counts (m, or NULL) receives how many rows
  * chose each expert.  Options out of range return SK_ERR_ROUTE.

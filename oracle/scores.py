@@ -74,7 +74,7 @@ def route(scores, k, fn="softmax", bias=None, select_on="score", n_group=1, topk
     """(idx, weights, counts)."""
     s = np.asarray(scores, np.float64)
     n, m = s.shape
-    # softmax and sigmoid rise with the score: where they alone decide, the scores decide
+    # softmax and sigmoid rise with the score: where they alone decide, the scores decide (v is for the groups' sums)
     alone = bias is None and (n_group == 1 or group_top == 1)
     v = s if alone else route_values(s, fn, bias, select_on)
     if n_group > 1:
@@ -82,6 +82,8 @@ def route(scores, k, fn="softmax", bias=None, select_on="score", n_group=1, topk
         score = np.sort(per, axis=2)[:, :, -group_top:].sum(axis=2)
         keep = np.zeros((n, n_group), bool)
         np.put_along_axis(keep, _order(score, topk_group), True, axis=1)
+        if bias is None:
+            v = s
         # columns of the other groups rank behind everything, masked ones included
         rank = np.empty((n, m), np.int64)
         np.put_along_axis(rank, _order(v, m), np.arange(m)[None, :].repeat(n, 0), axis=1)

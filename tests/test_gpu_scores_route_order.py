@@ -116,3 +116,19 @@ def test_score_and_bias_beyond_float32(sign, m, k):
     if m % 4 == 0 and k <= m // 2:
         for gt in (1, 2):
             same_choice(s, k, select_on="logit", bias=bias, n_group=4, topk_group=2, group_top=gt)
+
+
+@pytest.mark.parametrize("fn,step", [("sigmoid", 5.0), ("softmax", -800.0)])
+@pytest.mark.parametrize("m", [8, 48, 300])
+def test_saturated_acts_tie_under_a_bias_and_keep_the_scores_order_without_one(m, fn, step):
+    """Sigmoids that are 1, or softmax acts that are 0, in float64 too."""
+    s = (40.0 + step * (np.arange(m) % 6))[None, :].repeat(20, 0).astype(F)
+    if fn == "softmax":
+        s[:, m // 2] = 5000.0
+    x, k = torch.from_numpy(s).to(DEV), min(m // 4, 6)
+    for bias in (None, np.zeros(m, F), np.full(m, 0.25, F)):
+        same_choice(s, k, score_fn=fn, bias=bias)
+        same_choice(s, k, score_fn=fn, bias=bias, n_group=2, topk_group=1, group_top=2)
+    none, zero = (sk.scores_route(x, k, score_fn=fn, bias=b).idx[0].tolist() for b in (None, torch.zeros(m, device=DEV)))
+    assert none == np.argsort(-s[0], kind="stable")[:k].tolist()
+    assert zero == (list(range(k)) if fn == "sigmoid" else [m // 2] + list(range(k - 1)))
