@@ -327,19 +327,24 @@ __global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
                 A.counts[j] = 0;  // cleared here for the kernel that counts
         }
     }
-    // a finite bias that may take the sum with a finite score out of the float32 range (by half its last step, 2^103)
+    // Whether a finite bias may take its sum with a finite score out of the float32 range (by half its last step, 2^103).
     bool huge = false;
     for (int j = threadIdx.x; j < L * E; j += kBlock) {
         const float b = A.bias && j < A.m ? A.bias[j] : 0.0f;
         bias[j] = b;
         huge = huge || (fabsf(b) >= 0x1p102f && fabsf(b) < INFINITY);
     }
-    huge = __any(huge);
-    if (lane == 0) wave_huge[threadIdx.x / 64] = huge ? 1 : 0;
+    const bool sums = A.raw && A.bias;
+    if (sums) {
+        const bool any = __any(huge);
+        if (lane == 0) wave_huge[threadIdx.x / 64] = any ? 1 : 0;
+    }
     __syncthreads();
     huge = false;
+    if (sums) {
 #pragma unroll
-    for (int w = 0; w < kBlock / 64; ++w) huge = huge || wave_huge[w] != 0;
+        for (int w = 0; w < kBlock / 64; ++w) huge = huge || wave_huge[w] != 0;
+    }
     const int left = A.n_group > 1 ? A.topk_group * A.group_size : A.m;
     // where values are rounded, one more than k shows whether the last one chosen is apart from the first left out
     const bool check = A.doubt && A.bias;
@@ -371,7 +376,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_route(RouteArgs A) {
             key[e] = j < A.m ? key_of(choice_value<float>(A, s[e], bias[j], M, inv_S)) : NAN;
         }
         bool close = false;
-        if (huge && A.raw) {  // sums that are finite, whatever float32 makes of them, are left to float64
+        if (huge) {  // sums that are finite, whatever float32 makes of them, are left to float64
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 close = close || (fabsf(key[e]) == INFINITY && fabsf(s[e]) < INFINITY && fabsf(bias[Rw::col(e, l)]) < INFINITY);
