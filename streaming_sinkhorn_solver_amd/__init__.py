@@ -16,6 +16,11 @@ Potentials are returned in cost units (f, g), not divided by eps.
 The scores_* functions take a score matrix instead of clouds, (n, m) float32,
 bfloat16 or float16 with any row stride: balancing potentials and routing of a
 router's scores, log-probabilities of a head's, and their gradients.
+
+No function here takes part in autograd: inputs are read and outputs written by
+their addresses, so a result carries no graph, also where an input requires a
+gradient, and a tensor written into (``out``, ``grad``, ``g``, ...) keeps its version.
+A trainer wraps a forward and its gradient in a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
@@ -638,7 +643,8 @@ def scores_solve(scores, a=None, b=None, *, eps: float, n_iters: int, g_init: to
 
     For a router, rows are tokens (a: zero for padding) and columns experts (b: their capacities); a and b default
     to uniform weights.  g (plus eps * log b where b is not uniform) is the bias for balance that ``scores_route``
-    takes with select_on="logit".  g_init may be g itself.  With check, given weights are validated as in
+    takes with select_on="logit".  g_init may be g itself.  An expert is best switched off by b = 0: a column masked by
+    -inf in every row is summed anew in every iteration.  With check, given weights are validated as in
     ``check_inputs`` (this waits for the stream)."""
     s, code, n, m, ld = _scores(scores)
     a, b = _vec(a, n, torch.float32, s.device, "a"), _vec(b, m, torch.float32, s.device, "b")
@@ -758,7 +764,8 @@ def scores_logprobs_grad(scores, targets: torch.Tensor | None, fwd: Logprobs, *,
                          d_entropy: torch.Tensor | None = None, d_top: torch.Tensor | None = None,
                          grad: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of ``scores_logprobs`` in the scores from the gradients of its outputs (each optional; d_top is that
-    of top_logp); fwd is its result for the same scores, targets and eps.  grad may be scores itself."""
+    of top_logp); fwd is its result for the same scores, targets and eps.  grad may be scores itself; for a window of
+    padded rows a grad of the same row stride is written fastest (a new one is contiguous)."""
     s, code, n, m, ld = _scores(scores)
     dev = s.device
     targets = _vec(targets, n, torch.int64, dev, "targets")

@@ -478,7 +478,10 @@ struct LpGradArgs {
 // a0 = d_lse - sum of the picks' d - d_H (H - log S).
 // One pass: a thread loads and stores the same entries (so the gradient may
 // take the scores' place); the picks are put in afterwards by the workgroup
-// whose chunk they lie in.
+// whose chunk they lie in.  Rows whose scores and gradient lie differently to 16
+// bytes go entry by entry: 4096 rows of 50257 bf16 scores out of 50304 take 400 us
+// into a gradient of 50257, 152 into one of the scores' own row stride (7 rows of 8
+// of the former are such rows), 144 in place.
 template <class T, int NV>
 __global__ __launch_bounds__(kBlock) void k_logprobs_grad(LpGradArgs A) {
     constexpr int VE = Vec<T>::n;

@@ -13,7 +13,7 @@
 // crowd into a few lanes, take k rounds of an argmax (16384 x 256, k = 8: 30 us in
 // rounds alone, 14 ranked; with k = 16 of 16 lanes, where the bound is not used, 23).
 // The kernel is bound by latency and issue, not by the 16.8 MB that it reads: about
-// 600 vector instructions per wave of four rows.
+// 650 vector instructions per wave of four rows.
 //
 // The order of two values that are closer than the float32 rounding of act or
 // of the sum with the bias would depend on that rounding.  The choice is
@@ -667,7 +667,11 @@ __global__ __launch_bounds__(kBlock) void k_route_grad(RouteGradArgs A) {
     }
 }
 
-// f(lanes per row, scores per lane) for rows of m scores: as few lanes as hold the row at 16 scores each or less.
+// f(lanes per row, scores per lane) for rows of m scores.  8 scores per lane up to 128 columns: with half the lanes and
+// 16 scores each, 32768 x 64 f32, k = 6 takes 14.0 us and one row 7.2, against 13.6 and 5.7 so; 32768 x 128 bf16, k = 8
+// takes 17.7 and one row 7.4, against 18.7 and 5.7.  256 columns take 16 x 16 (14 us; 32 x 8 takes 27).  For 257 to 512
+// columns 64 x 8 is the shorter for one row (6.2 us; 32 x 16: 6.6) and the longer for many: 16384 x 512 f32, k = 8
+// takes 27 us, 21 with 32 x 16.
 template <class F>
 void by_width(int m, F f) {
     using std::integral_constant;
