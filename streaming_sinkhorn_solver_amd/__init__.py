@@ -677,8 +677,8 @@ def scores_route(scores, k: int, *, score_fn: str = "softmax", bias: torch.Tenso
 
     The choice is by softmax or sigmoid of the scores (select_on="score"), or by the scores themselves ("logit"),
     plus bias (m,), in the order of these values in float64 (without a bias in that of the scores themselves); with
-    n_group > 1 inside the topk_group best groups of columns (by the sum of a group's group_top largest values).  The weights are the softmax or sigmoid at the choice, divided by their sum with renorm, times
-    scale.  ``out``: a Routing of earlier buffers to write into."""
+    n_group > 1 inside the topk_group best groups of columns (by the sum of a group's group_top largest values).  The
+    weights are the softmax or sigmoid at the choice, divided by their sum with renorm, times scale.  ``out``: a Routing of earlier buffers to write into."""
     if score_fn not in SCORE_FNS or select_on not in SELECT_ON:
         raise ValueError(f"score_fn must be one of {list(SCORE_FNS)}, select_on one of {list(SELECT_ON)}")
     s, code, n, m, ld = _scores(scores)
