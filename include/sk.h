@@ -85,8 +85,8 @@ typedef enum sk_status {
     SK_ERR_SCRATCH = 17,       /* sk_solve_noalloc: sk_workspace_bytes(n, m, d) exceeds
                                   SK_NOALLOC_SCRATCH_BYTES */
     SK_ERR_DTYPE = 18,         /* unknown element type, or an address not aligned to its elements */
-    SK_ERR_ROUTE = 19,         /* a routing option out of range (see sk_scores_route) */
-    SK_ERR_OVERLAP = 20        /* a gradient that overlaps the scores without taking their place */
+    SK_ERR_ROUTE = 19,         /* a routing option out of range (see sk_scores_route, sk_route_sort) */
+    SK_ERR_OVERLAP = 20        /* an output that overlaps an input without taking its place */
 } sk_status;
 
 /* Element types of a score matrix. */
@@ -568,6 +568,109 @@ int sk_scores_logprobs_grad(const void *scores, int32_t dtype, int64_t n, int64_
                             const float *entropy, int32_t top, const int32_t *top_idx,
                             const float *d_logp, const float *d_lse, const float *d_entropy,
                             const float *d_top, void *grad, int64_t ld_grad, void *stream);
+
+/*
+ * Drafted tokens against the target's probabilities, from given random numbers.
+ * Request r of b has rows starts[r] to starts[r + 1] - 1 (starts: b + 1 nondecreasing
+ * int64; taken into [0, n]) of scores, the target's, with p = softmax(s / eps);
+ * eps = 0 is greedy, p one at the row's largest score, the first of equal ones.
+ * tokens (n int64): the token drafted at the row, negative: none, which ends the
+ * request.  draft: the scores they were drawn from, q = softmax(t / eps_draft), of the
+ * scores' type and size, row stride ld_draft (rows without a drafted token are not
+ * read), or NULL: q is one at the drafted token.  n, b >= 0, m <= 2^30.
+ * A request takes the drafted tokens x of its rows while u_accept[i] q_i(x) < p_i(x),
+ * and stops at the first row that is not taken or has none.  There it draws
+ *     next = min { j : sum_{l <= j} w_l > u_sample[r] sum_l w_l },
+ *     w = max(p - q, 0), or p where no token was drafted (or p - q leaves nothing),
+ * so that what it emits is distributed as p (the maximal coupling of p and q).
+ * u_accept (n) and u_sample (b) are float32 from [0, 1) (NULL where eps = 0).
+ *     accepted (b): drafted tokens taken;  next (b int64): the token drawn, -1: none
+ *                  (all rows taken, no row, or nothing to draw from);
+ *     out_tokens (n int64): what each row emits, drafted tokens taken, then next, then -1;
+ *     ratio (n):   min(1, p_i(x) / q_i(x)) of every drafted token, also behind the stop;
+ *                  0 at and behind the request's row without one;
+ *     logp (n):    log p_i of the token emitted; 0 where none is.
+ * Rows of no request are left as they are.  out_tokens may be tokens.  A drafted token
+ * >= m is not taken; a masked one (p = 0) neither; one with q = 0 < p is.  A row that the
+ * mask leaves empty takes nothing and draws nothing (-1).  A NaN or +inf score, of the draft
+ * too, makes its row's ratio NaN (not taken) and nothing is drawn there.  Exponentials, sums
+ * and comparisons are float64 and probabilities below 2^-1000 count as 0, so decisions and
+ * draws are those of the exact probabilities but within some 2^-45 of a border.
+ */
+size_t sk_scores_verify_workspace_bytes(int32_t dtype, int64_t n, int64_t m, int64_t b);
+int sk_scores_verify(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,
+                     float eps, const void *draft, int64_t ld_draft, float eps_draft,
+                     const int64_t *tokens, const int64_t *starts, int64_t b,
+                     const float *u_accept, const float *u_sample,
+                     int32_t *accepted, int64_t *next, int64_t *out_tokens,
+                     float *ratio, float *logp, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * ----- Token rows under a routing ---------------------------------------------
+ *
+ * What follows sk_scores_route: its choices sorted by expert, token rows brought into
+ * that order, the experts' rows summed back, and the gradients.  A choice (i, r) of idx
+ * (n, k) is numbered i k + r; k <= 64, m <= 1024 experts.  Token matrices are (n, d),
+ * sorted ones (rows, d), of one sk_dtype, each with its own row stride >= d and
+ * aligned to its elements (any address and stride otherwise).  Products and sums are float32,
+ * rounded once on output.  Outputs must not overlap inputs but where stated
+ * (SK_ERR_OVERLAP).  Results are deterministic; all calls enqueue only (capturable).
+ */
+
+/* Rows of n tokens' sorted choices at most: n k and every segment's padding, or m whole capacities where that is
+   less; -1 for invalid arguments or beyond 2^31 - 1. */
+int64_t sk_route_sort_rows(int64_t n, int32_t k, int64_t m, int32_t align, int32_t capacity);
+
+/* Workspace bytes of sk_route_sort (0 for invalid sizes). */
+size_t sk_route_sort_workspace_bytes(int64_t n, int32_t k, int64_t m);
+
+/*
+ * The choices sorted by expert, those of one expert in the order of their numbers.
+ * Choices outside [0, m) are dropped, and with capacity > 0 those of an expert after
+ * its first `capacity`.  counts (m): rows of each expert; offsets (m + 1): its first
+ * row, a multiple of align >= 1; offsets[m] is the end of the last segment.
+ * slot (n, k): the row of each choice, -1: dropped.  source (rows): the choice of each
+ * row, -1: none (a segment's padding, and all rows from offsets[m] on); rows >=
+ * sk_route_sort_rows(n, k, m, align, capacity).
+ */
+int sk_route_sort(const int32_t *idx, int64_t n, int32_t k, int64_t m, int32_t align, int32_t capacity,
+                  int32_t *slot, int32_t *source, int64_t rows, int32_t *counts, int32_t *offsets,
+                  void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Token rows to the experts: out[slot[i, r]] = x[i], times weights[i, r] where weights
+ * (n, k) are given.  Slots outside [0, rows) are dropped.  With counts (m) and offsets
+ * (m + 1) given the padding of the segments becomes zero; both NULL where there is none.  Rows from
+ * offsets[m] on are left as they are.
+ */
+int sk_route_dispatch(const void *x, int32_t dtype, int64_t n, int64_t d, int64_t ld,
+                      const int32_t *slot, int32_t k, const float *weights,
+                      const int32_t *counts, const int32_t *offsets, int64_t m,
+                      void *out, int64_t rows, int64_t ld_out, void *stream);
+
+/*
+ * The experts' rows back to the tokens:
+ *     y[i] = add[i] + sum_r weights[i, r] in[slot[i, r]],
+ * in the order of r; weights NULL: 1, add NULL: 0; dropped choices have no part (also
+ * where their weight is NaN).  add may be y (same stride).  Without weights this is the gradient of
+ * sk_route_dispatch, with them that of the weighted one.
+ */
+int sk_route_combine(const void *in, int32_t dtype, int64_t rows, int64_t d, int64_t ld_in,
+                     const int32_t *slot, int64_t n, int32_t k, const float *weights,
+                     const void *add, int64_t ld_add, void *y, int64_t ld_y, void *stream);
+
+/*
+ * Gradient of sk_route_combine from d_y (n, d) (that of add is d_y itself):
+ *     d_rows[slot[i, r]] = weights[i, r] d_y[i],  d_weights[i, r] = <in[slot[i, r]], d_y[i]>,
+ * 0 for a dropped choice; padding and the rows behind as in sk_route_dispatch.  Either
+ * output may be NULL; without d_weights `in` is not read.  d_rows may be `in` (same stride).
+ * With in = the gradient of sk_route_dispatch's rows and d_y = x, d_weights is that of its weights.
+ */
+int sk_route_combine_grad(const void *in, int32_t dtype, int64_t rows, int64_t d, int64_t ld_in,
+                          const int32_t *slot, int64_t n, int32_t k, const float *weights,
+                          const int32_t *counts, const int32_t *offsets, int64_t m,
+                          const void *d_y, int64_t ld_dy, void *d_rows, int64_t ld_out,
+                          float *d_weights, void *stream);
 
 /*
  * Kernel timing of the streamed log-sum-exp passes (benchmark diagnostics).

@@ -102,6 +102,17 @@ SIGNATURES = {
                                           _vp, _sz, _vp]),
     "sk_scores_logprobs_grad": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
                                                _vp, _vp, _vp, _i64, _vp]),
+    "sk_scores_verify_workspace_bytes": (_sz, [_i32, _i64, _i64, _i64]),
+    "sk_scores_verify": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _i64, _f32, _vp, _vp, _i64, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sk_route_sort_rows": (_i64, [_i64, _i32, _i64, _i32, _i32]),
+    "sk_route_sort_workspace_bytes": (_sz, [_i64, _i32, _i64]),
+    "sk_route_sort": (ctypes.c_int, [_vp, _i64, _i32, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "sk_route_dispatch": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _i64, _vp, _i64, _i64,
+                                         _vp]),
+    "sk_route_combine": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "sk_route_combine_grad": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _vp, _i64,
+                                             _vp, _i64, _vp, _vp]),
     "sk_timing_enable": (ctypes.c_int, [ctypes.c_int]),
     "sk_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64),
                                       ctypes.POINTER(ctypes.c_double)]),
@@ -562,18 +573,18 @@ def grad_x(x, y, a, b, g, *, eps: float, ws: torch.Tensor | None = None,
     return out
 
 
-def _scores(scores):
+def _scores(scores, name: str = "scores", shape: str = "(n, m)"):
     """A score matrix as (tensor, dtype code, n, m, row stride): (n, m) float32, bfloat16 or float16 on a GPU, any
     row stride; scores whose neighbours in a row do not lie next to each other are copied."""
     if not isinstance(scores, torch.Tensor):
-        raise TypeError("scores must be a torch tensor")
+        raise TypeError(f"{name} must be a torch tensor")
     code = DTYPES.get(scores.dtype)
     if code is None:
-        raise ValueError(f"scores must be float32, bfloat16 or float16 (got {scores.dtype})")
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {scores.dtype})")
     if scores.dim() != 2:
-        raise ValueError(f"scores must be (n, m) (got shape {tuple(scores.shape)})")
+        raise ValueError(f"{name} must be {shape} (got shape {tuple(scores.shape)})")
     if scores.device.type != "cuda":
-        raise ValueError("scores must be on a GPU device")
+        raise ValueError(f"{name} must be on a GPU device")
     n, m = scores.shape
     ld = scores.stride(0)
     if (m > 1 and scores.stride(1) != 1) or (n > 1 and ld < m):
@@ -789,6 +800,213 @@ def scores_logprobs_grad(scores, targets: torch.Tensor | None, fwd: Logprobs, *,
     return grad
 
 
+class Verified(NamedTuple):
+    """Of each request the number of drafted tokens taken (b,) int32 and the token drawn behind them (b,) int64 (-1:
+    none); of each row the token emitted there (n,) int64 (-1: none), min(1, p/q) of its drafted token and the
+    log-probability of the emitted one, (n,) float32 (0: none)."""
+    accepted: torch.Tensor
+    next: torch.Tensor
+    tokens: torch.Tensor
+    ratio: torch.Tensor
+    logp: torch.Tensor
+
+
+def scores_verify_workspace(dtype: torch.dtype, n: int, m: int, b: int, device) -> torch.Tensor:
+    """A workspace tensor for scores_verify of b requests on an (n, m) score matrix of this dtype."""
+    nb = int(load_library().sk_scores_verify_workspace_bytes(DTYPES.get(dtype, -1), n, m, b))
+    if nb == 0:
+        raise ValueError(f"invalid arguments for scores_verify (dtype={dtype} n={n} m={m} b={b}: m <= 2**30)")
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def scores_verify(scores, tokens: torch.Tensor, starts: torch.Tensor, u_accept: torch.Tensor | None,
+                  u_sample: torch.Tensor | None, *, draft: torch.Tensor | None = None, eps: float = 1.0,
+                  eps_draft: float = 1.0, ws: torch.Tensor | None = None, out: Verified | None = None) -> Verified:
+    """Drafted tokens against the target's probabilities p = softmax(scores / eps), from given random numbers.
+
+    Request r's rows of scores are starts[r] to starts[r + 1] - 1 (starts: (b + 1,) int64); each is the target's
+    distribution of the token after those before it, and tokens (n,) int64 the token drafted there (negative: none, which
+    ends the request; usually its last row).  draft: the scores that the tokens were drawn from, q = softmax(draft /
+    eps_draft), of the scores' type and shape (rows without a drafted token are not read), or None where each token was
+    proposed with certainty.  From its first row on a request takes drafted tokens while u_accept * q(token) < p(token);
+    where it stops it draws from max(p - q, 0), or from p where no token was drafted, by u_sample (b,): the first column
+    whose cumulative weight exceeds u_sample of the whole.  The emitted tokens are then distributed as p.  u_accept (n,)
+    and u_sample are float32 from [0, 1); eps = 0 is greedy (the largest score, the first of equal ones, has p = 1) and
+    needs neither.  Decisions and draws are made in float64.  ``out``: a Verified of earlier buffers to write into; its
+    tokens may be the tokens given."""
+    s, code, n, m, ld = _scores(scores)
+    dev = s.device
+    if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must be a (b + 1,) int64 tensor")
+    b = starts.shape[0] - 1
+    starts, tokens = _vec(starts, b + 1, torch.int64, dev, "starts"), _vec(tokens, n, torch.int64, dev, "tokens")
+    u_accept, u_sample = _vec(u_accept, n, torch.float32, dev, "u_accept"), _vec(u_sample, b, torch.float32, dev, "u_sample")
+    if tokens is None or (eps != 0 and (u_accept is None or u_sample is None)):
+        raise ValueError("tokens, and unless eps is 0 u_accept and u_sample, must be given")
+    ld_q = ld
+    if draft is not None:
+        draft, code_q, nq, mq, ld_q = _scores(draft, "draft")
+        if code_q != code or (nq, mq) != (n, m) or draft.device != dev:
+            raise ValueError(f"draft must be a {s.dtype} tensor of shape {(n, m)} on {dev}")
+    ws = _ws(ws, dev, lambda: scores_verify_workspace(s.dtype, n, m, b, dev))
+    o_acc, o_next, o_tok, o_ratio, o_logp = out or (None,) * 5
+    acc = _out(o_acc, (b,), torch.int32, dev, "out.accepted")
+    nxt = _out(o_next, (b,), torch.int64, dev, "out.next")
+    tok = _out(o_tok, (n,), torch.int64, dev, "out.tokens")
+    ratio = _out(o_ratio, (n,), torch.float32, dev, "out.ratio")
+    logp = _out(o_logp, (n,), torch.float32, dev, "out.logp")
+    _call("sk_scores_verify", dev, s.data_ptr(), code, n, m, ld, float(eps), _addr(draft), ld_q, float(eps_draft),
+          tokens.data_ptr(), starts.data_ptr(), b, _addr(u_accept), _addr(u_sample), acc.data_ptr(), nxt.data_ptr(),
+          tok.data_ptr(), ratio.data_ptr(), logp.data_ptr(), ws.data_ptr(), ws.numel())
+    return Verified(acc, nxt, tok, ratio, logp)
+
+
+class RoutePlan(NamedTuple):
+    """Where each choice's row lies: slot (n, k) int32, the row of choice (i, r), -1 where it was dropped; source (rows,)
+    int32, the choice i * k + r of a row, -1 of none; counts (m,) int32, rows of each expert; offsets (m + 1,) int32, its
+    first row (a multiple of align), the last entry the end of all."""
+    slot: torch.Tensor
+    source: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    align: int = 1
+
+
+def route_sort_rows(n: int, k: int, m: int, align: int = 1, capacity: int = 0) -> int:
+    """Rows that the sorted choices of n tokens can take at most (the length of a plan's source)."""
+    rows = int(load_library().sk_route_sort_rows(n, k, m, align, capacity))
+    if rows < 0:
+        raise ValueError(f"invalid arguments for route_sort (n={n} k={k} m={m} align={align} capacity={capacity}: "
+                         "1 <= k <= 64, 1 <= m <= 1024, align >= 1, capacity >= 0, fewer than 2**31 rows)")
+    return rows
+
+
+def route_sort_workspace(n: int, k: int, m: int, device) -> torch.Tensor:
+    """A workspace tensor for route_sort of (n, k) choices among m experts."""
+    nb = int(load_library().sk_route_sort_workspace_bytes(n, k, m))
+    if nb == 0:
+        raise ValueError(f"invalid problem size n={n} k={k} m={m} (1 <= k <= 64, 1 <= m <= 1024, n * k < 2**31)")
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def route_sort(idx: torch.Tensor, m: int, *, align: int = 1, capacity: int = 0, ws: torch.Tensor | None = None,
+               out: RoutePlan | None = None) -> RoutePlan:
+    """The choices idx (n, k) int32 of ``scores_route`` sorted by expert, in the order of the tokens inside each.
+
+    Choices outside [0, m) are dropped (experts of other devices), and with a capacity those of an expert beyond its
+    first ``capacity``.  Every expert's rows start at a multiple of align.  ``out``: a RoutePlan of earlier buffers to
+    write into (its source of route_sort_rows(n, k, m, align, capacity) entries or more)."""
+    if not isinstance(idx, torch.Tensor):
+        raise TypeError("idx must be a torch tensor")
+    if idx.dtype != torch.int32 or idx.dim() != 2:
+        raise ValueError(f"idx must be an (n, k) int32 tensor (got {idx.dtype} of shape {tuple(idx.shape)})")
+    dev = idx.device
+    if dev.type != "cuda":
+        raise ValueError("idx must be on a GPU device")
+    n, k = idx.shape
+    m, align, capacity = int(m), int(align), int(capacity)
+    rows = route_sort_rows(n, k, m, align, capacity)
+    idx = idx.contiguous()
+    ws = _ws(ws, dev, lambda: route_sort_workspace(n, k, m, dev))
+    o_slot, o_source, o_counts, o_offsets, _ = out or (None,) * 5
+    slot = _out(o_slot, (n, k), torch.int32, dev, "out.slot")
+    source = torch.empty(rows, dtype=torch.int32, device=dev) if o_source is None else _at_least(
+        o_source, rows, torch.int32, dev, "out.source")
+    counts = _out(o_counts, (m,), torch.int32, dev, "out.counts")
+    offsets = _out(o_offsets, (m + 1,), torch.int32, dev, "out.offsets")
+    _call("sk_route_sort", dev, idx.data_ptr(), n, k, m, align, capacity, slot.data_ptr(), source.data_ptr(),
+          source.numel(), counts.data_ptr(), offsets.data_ptr(), ws.data_ptr(), ws.numel())
+    return RoutePlan(slot, source, counts, offsets, align)
+
+
+def _plan(plan, device):
+    """A plan as (slot, k, n, rows, counts, offsets, m): counts and offsets only where segments are padded."""
+    slot = plan.slot
+    if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
+        raise ValueError("plan.slot must be an (n, k) int32 tensor")
+    n, k = slot.shape
+    slot = _vec(slot, (n, k), torch.int32, device, "plan.slot")
+    if plan.align <= 1:
+        return slot, k, n, plan.source.shape[0], None, None, 0
+    m = plan.counts.shape[0]
+    return (slot, k, n, plan.source.shape[0], _vec(plan.counts, m, torch.int32, device, "plan.counts"),
+            _vec(plan.offsets, m + 1, torch.int32, device, "plan.offsets"), m)
+
+
+def _row_buf(t, shape, like, name):
+    """A caller's (rows, d) output of like's type with contiguous rows, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if not isinstance(t, torch.Tensor) or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
+    if tuple(t.shape) != shape or (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise ValueError(f"{name} must be {shape} with contiguous rows (got {tuple(t.shape)})")
+    return t
+
+
+def route_dispatch(x, plan: RoutePlan, weights: torch.Tensor | None = None, *, out: torch.Tensor | None = None):
+    """Token rows x (n, d) in the plan's order: (rows, d) of x's type, rows[slot[i, r]] = x[i], times weights[i, r] where
+    weights (n, k) float32 are given.  A segment's padding is zero; rows behind the last segment (plan.offsets[m]) are
+    left as they are in ``out``, unset in a new tensor.  Its gradient in x is ``route_combine(d_rows, plan, weights)``,
+    that in the weights ``route_combine_grad(d_rows, plan, None, x, rows_grad=False)``."""
+    x, code, n, d, ld = _scores(x, "x", "(n, d)")
+    slot, k, pn, rows, counts, offsets, m = _plan(plan, x.device)
+    if pn != n:
+        raise ValueError(f"x must have the plan's {pn} tokens (got {n})")
+    weights = _vec(weights, (n, k), torch.float32, x.device, "weights")
+    out = _row_buf(out, (rows, d), x, "out")
+    _call("sk_route_dispatch", x.device, x.data_ptr(), code, n, d, ld, slot.data_ptr(), k, _addr(weights), _addr(counts),
+          _addr(offsets), m, out.data_ptr(), rows, max(out.stride(0), d))
+    return out
+
+
+def route_combine(rows, plan: RoutePlan, weights: torch.Tensor | None = None, *, add: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None):
+    """The experts' rows (rows, d) summed back onto their tokens: y (n, d) of the rows' type, y[i] = add[i] + sum over r of
+    weights[i, r] * rows[slot[i, r]], in float32, rounded once; weights (n, k) float32 default to 1, dropped choices have
+    no part.  add (n, d) may be ``out`` itself.  Without weights this is the gradient of ``route_dispatch``."""
+    rows, code, nr, d, ld = _scores(rows, "rows", "(rows, d)")
+    dev = rows.device
+    slot, k, n, pr, _, _, _ = _plan(plan, dev)
+    if nr != pr:
+        raise ValueError(f"rows must have the plan's {pr} rows (got {nr})")
+    weights = _vec(weights, (n, k), torch.float32, dev, "weights")
+    ld_add = d
+    if add is not None:
+        add, code_add, na, da, ld_add = _scores(add, "add", "(n, d)")
+        if code_add != code or (na, da) != (n, d) or add.device != dev:
+            raise ValueError(f"add must be a {rows.dtype} tensor of shape {(n, d)} on {dev}")
+    out = _row_buf(out, (n, d), rows, "out")
+    _call("sk_route_combine", dev, rows.data_ptr(), code, nr, d, ld, slot.data_ptr(), n, k, _addr(weights), _addr(add), ld_add,
+          out.data_ptr(), max(out.stride(0), d))
+    return out
+
+
+def route_combine_grad(rows, plan: RoutePlan, weights: torch.Tensor | None, d_y, *, rows_grad: bool = True,
+                       weights_grad: bool = True, d_rows: torch.Tensor | None = None,
+                       d_weights: torch.Tensor | None = None):
+    """Gradients of ``route_combine`` from d_y (n, d): (d_rows (rows, d), d_weights (n, k) float32), either None where it is
+    not asked for.  d_rows has the padding and the rest of ``route_dispatch``'s rows and may be rows itself; that of add is
+    d_y.  Without weights_grad rows are not read."""
+    rows, code, nr, d, ld = _scores(rows, "rows", "(rows, d)")
+    dev = rows.device
+    slot, k, n, pr, counts, offsets, m = _plan(plan, dev)
+    d_y, code_y, ny, dy, ld_y = _scores(d_y, "d_y", "(n, d)")
+    if nr != pr:
+        raise ValueError(f"rows must have the plan's {pr} rows (got {nr})")
+    if code_y != code or (ny, dy) != (n, d) or d_y.device != dev:
+        raise ValueError(f"d_y must be a {rows.dtype} tensor of shape {(n, d)} on {dev}")
+    if not rows_grad and not weights_grad:
+        raise ValueError("rows_grad or weights_grad must be asked for")
+    weights = _vec(weights, (n, k), torch.float32, dev, "weights")
+    d_rows = _row_buf(d_rows, (nr, d), rows, "d_rows") if rows_grad else None
+    d_weights = _out(d_weights, (n, k), torch.float32, dev, "d_weights") if weights_grad else None
+    _call("sk_route_combine_grad", dev, rows.data_ptr(), code, nr, d, ld, slot.data_ptr(), n, k, _addr(weights),
+          _addr(counts), _addr(offsets), m, d_y.data_ptr(), ld_y, _addr(d_rows), max(d_rows.stride(0), d) if rows_grad else d,
+          _addr(d_weights))
+    return d_rows, d_weights
+
+
 def timing_enable(enable: bool = True, stride: int = 1) -> None:
     """Start (reset) or stop event timing of the streamed-pass kernels; every
     stride-th pass launch is timed."""
@@ -810,4 +1028,6 @@ __all__ = ["timing_enable", "timing_read", "solve", "solve_ex", "gradient_flow",
            "load_library", "status_string", "SinkhornError", "LIB_PATH", "SIGNATURES", "VARIANTS", "STOP_MODES",
            "solve_noalloc", "NOALLOC_SCRATCH_BYTES", "solve_warm", "primal_cost",
            "scores_solve", "scores_solve_workspace", "scores_route", "scores_route_grad", "Routing", "scores_logprobs",
-           "scores_logprobs_grad", "scores_logprobs_workspace", "Logprobs", "DTYPES", "SCORE_FNS", "SELECT_ON"]
+           "scores_logprobs_grad", "scores_logprobs_workspace", "Logprobs", "DTYPES", "SCORE_FNS", "SELECT_ON",
+           "scores_verify", "scores_verify_workspace", "Verified", "route_sort", "route_sort_rows", "route_sort_workspace",
+           "RoutePlan", "route_dispatch", "route_combine", "route_combine_grad"]

@@ -1407,8 +1407,8 @@ const char* sk_status_string(int status) {
         case SK_ERR_DTYPE: return "unknown element type, or an address not aligned to its elements";
         case SK_ERR_ROUTE:
             return "a routing option is out of range (groups divide m, topk_group <= n_group, group_top 1 or 2, "
-                   "k <= 64 within the chosen groups)";
-        case SK_ERR_OVERLAP: return "the gradient overlaps the scores without taking their place";
+                   "k <= 64 within the chosen groups, align >= 1, capacity >= 0)";
+        case SK_ERR_OVERLAP: return "an output overlaps an input without taking its place";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,643 @@
+// sk_route_rows.hip -- token rows under a routing: the choices sorted by expert
+// (sk_route_sort), token rows copied into that order (sk_route_dispatch), the
+// experts' rows summed back onto their tokens (sk_route_combine), and the
+// gradient of that sum (sk_route_combine_grad).
+//
+// A choice, or pair, t = i k + r is the r-th expert of token i.  The plan is a
+// 0/1 matrix with one entry per pair; dispatch applies it, combine its transpose,
+// both with the routing's weights or without.
+#include "sk_scores.hpp"
+
+#include <algorithm>
+
+namespace sk {
+namespace {
+
+constexpr int kRowsMaxExperts = 1024;
+constexpr int kRowsMaxTop = 64;
+
+// ----- the choices sorted by expert ---------------------------------------------------
+// A stable counting sort.  A wave takes its pairs 64 at a time, in order; lanes of
+// equal expert find one another by one ballot per bit of its number, so a pair's rank
+// among the wave's pairs of its expert is a count of lower lanes beside the wave's own
+// counter in LDS.  Adding the counts of the waves and workgroups before gives the rank
+// among all.
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortMost = 16;      // pairs per thread at most: a wave's counter fits 16 bits
+constexpr int kSortOne = 4096;     // pairs that one workgroup takes alone
+constexpr int kSortGroups = 64;    // workgroups whose counts the others add up themselves
+
+struct SortArgs {
+    const int32_t* idx;
+    int64_t pairs, rows;
+    int m, bits, align, capacity;
+    int per;  // pairs of a workgroup
+    int groups, scanned;
+    int32_t *slot, *source, *counts, *offsets;
+    int32_t* hist;  // [groups][m] counts of the workgroups (scanned: of those before), then [m] totals
+};
+
+__device__ __forceinline__ int expert_of(const SortArgs& A, int64_t t) {
+    const int e = t < A.pairs ? A.idx[t] : A.m;
+    return (unsigned)e < (unsigned)A.m ? e : A.m;  // m: dropped
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs A) {
+    __shared__ int hist[kRowsMaxExperts];
+    for (int e = threadIdx.x; e < A.m; e += kSortThreads) hist[e] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * A.per;
+    for (int q = threadIdx.x; q < A.per; q += kSortThreads) {
+        const int e = expert_of(A, t0 + q);
+        if (e < A.m) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < A.m; e += kSortThreads) A.hist[(int64_t)blockIdx.x * A.m + e] = hist[e];
+}
+
+// Counts of each workgroup to those of the workgroups before it, 64 experts per workgroup.
+__global__ __launch_bounds__(kSortThreads) void k_sort_scan(SortArgs A) {
+    __shared__ int part[kSortWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, e = blockIdx.x * 64 + lane;
+    const int64_t per = (A.groups + kSortWaves - 1) / kSortWaves;
+    const int64_t g0 = min(per * wave, (int64_t)A.groups), g1 = min(g0 + per, (int64_t)A.groups);
+    int sum = 0;
+    if (e < A.m)
+        for (int64_t g = g0; g < g1; ++g) sum += A.hist[g * A.m + e];
+    part[wave][lane] = sum;
+    __syncthreads();
+    int run = 0, total = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        run += w < wave ? part[w][lane] : 0;
+        total += part[w][lane];
+    }
+    if (e >= A.m) return;
+    for (int64_t g = g0; g < g1; ++g) {
+        const int here = A.hist[g * A.m + e];
+        A.hist[g * A.m + e] = run;
+        run += here;
+    }
+    if (wave == 0) A.hist[(int64_t)A.groups * A.m + e] = total;
+}
+
+template <int J>
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs A) {
+    __shared__ uint16_t count[kSortWaves][kRowsMaxExperts];  // then: of the waves before
+    __shared__ int first[kRowsMaxExperts], stop[kRowsMaxExperts], before[kRowsMaxExperts];
+    __shared__ int sums[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, group = blockIdx.x;
+    for (int e = lane; e < A.m; e += 64) count[wave][e] = 0;
+    wave_sync();
+    const int64_t t0 = (int64_t)group * A.per + wave * (64 * J) + lane;
+    int e[J], rank[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) e[j] = expert_of(A, t0 + j * 64);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        uint64_t same = ~0ull;
+        for (int b = 0; b < A.bits; ++b) {
+            const bool set = e[j] >> b & 1;
+            const uint64_t with = __ballot(set);
+            same &= set ? with : ~with;
+        }
+        const int lower = __popcll(same & ((1ull << lane) - 1));
+        rank[j] = lower + (e[j] < A.m ? count[wave][e[j]] : 0);
+        wave_sync();
+        if (e[j] < A.m && (same >> lane) == 1) count[wave][e[j]] = (uint16_t)(rank[j] + 1);  // the highest of them
+        wave_sync();
+    }
+    __syncthreads();
+    // each thread an expert: its pairs in this workgroup, in those before, in all; then the segments' first rows
+    int total = 0, kept = 0, padded = 0;
+    if (tid < A.m) {
+        int run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int here = count[w][tid];
+            count[w][tid] = (uint16_t)run;
+            run += here;
+        }
+        int prior = 0;
+        if (A.groups == 1) {
+            total = run;
+        } else if (A.scanned) {
+            prior = A.hist[(int64_t)group * A.m + tid];
+            total = A.hist[(int64_t)A.groups * A.m + tid];
+        } else {
+#pragma unroll 8
+            for (int g = 0; g < A.groups; ++g) {
+                const int here = A.hist[g * A.m + tid];
+                prior += g < group ? here : 0;
+                total += here;
+            }
+        }
+        before[tid] = prior;
+        kept = A.capacity ? min(total, A.capacity) : total;
+        padded = (int)(((int64_t)kept + A.align - 1) / A.align * A.align);
+    }
+    int upto = padded;
+    for (int o = 1; o < 64; o *= 2) {
+        const int low = __shfl_up(upto, o);
+        if (lane >= o) upto += low;
+    }
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    int end = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+        const int s = sums[w];
+        upto += w < wave ? s : 0;
+        end += s;
+    }
+    if (tid < A.m) {
+        first[tid] = upto - padded;
+        stop[tid] = upto - padded + kept;
+        if (group == 0) {
+            A.counts[tid] = kept;
+            A.offsets[tid + 1] = upto;
+            if (tid == 0) A.offsets[0] = 0;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int64_t t = t0 + j * 64;
+        if (t >= A.pairs) continue;
+        int at = -1;
+        if (e[j] < A.m) {
+            const int r = before[e[j]] + count[wave][e[j]] + rank[j];
+            if (!A.capacity || r < A.capacity) at = first[e[j]] + r;
+        }
+        A.slot[t] = at;
+        if (at >= 0) A.source[at] = (int32_t)t;
+    }
+    // rows of no pair: the segments' padding, and what lies behind the last segment
+    if (A.align > 1)
+        for (int q = group * kSortWaves + wave; q < A.m; q += A.groups * kSortWaves) {
+            const int next = q + 1 < A.m ? first[q + 1] : end;
+            for (int s = stop[q] + lane; s < next; s += 64) A.source[s] = -1;
+        }
+    for (int64_t s = end + (int64_t)group * kSortThreads + tid; s < A.rows; s += (int64_t)A.groups * kSortThreads) A.source[s] = -1;
+}
+
+template <int J>
+hipError_t launch_place(const SortArgs& A, hipStream_t s) {
+    hipLaunchKernelGGL((k_sort_place<J>), dim3((unsigned)A.groups), dim3(kSortThreads), 0, s, A);
+    return hipGetLastError();
+}
+
+// How the pairs are shared out: per workgroup a power-of-two number of pairs per thread.
+struct SortPlan {
+    int per_thread, groups;
+    size_t hist, total;
+};
+
+SortPlan sort_plan(int64_t pairs, int64_t m) {
+    SortPlan P{1, 1, 0, 256};
+    const int64_t most = pairs <= kSortOne ? 1 : kSortGroups;
+    while (P.per_thread < kSortMost && (int64_t)P.per_thread * kSortThreads * most < pairs) P.per_thread *= 2;
+    const int64_t per = (int64_t)P.per_thread * kSortThreads;
+    P.groups = (int)std::max<int64_t>(1, (pairs + per - 1) / per);
+    if (P.groups > 1) P.total = ((size_t)(P.groups + 1) * (size_t)m * 4 + 255) / 256 * 256;
+    return P;
+}
+
+// Rows of the sorted pairs at most, every segment rounded up to align; -1 for invalid arguments or beyond 2^31 - 1.
+int64_t sort_rows(int64_t n, int32_t k, int64_t m, int32_t align, int32_t capacity) {
+    if (n < 0 || n > INT32_MAX || k < 1 || k > kRowsMaxTop || m < 1 || m > kRowsMaxExperts || align < 1 || capacity < 0)
+        return -1;
+    const int64_t pairs = n * k;
+    int64_t rows = pairs + std::min(pairs, m) * ((int64_t)align - 1);
+    if (capacity) rows = std::min(rows, m * (((int64_t)capacity + align - 1) / align * align));
+    return rows <= INT32_MAX && pairs <= INT32_MAX ? rows : -1;
+}
+
+// ----- token rows -----------------------------------------------------------------------
+struct RowsArgs {
+    int64_t n, d, rows;
+    int k, m;
+    int lanes;           // of a token: a power of two up to the workgroup
+    int64_t runs, span;  // runs of 16 bytes of a row, and those that one workgroup takes
+    int64_t token_groups;  // groups of kBlock / lanes tokens
+    int64_t grid;          // workgroups that take them in turn
+    const int32_t *slot, *counts, *offsets;
+    const float* weights;
+    const void *tokens, *add, *in;  // (n, d); (n, d); (rows, d)
+    int64_t ld_tokens, ld_add, ld_in;
+    void* out;
+    int64_t ld_out;
+    float* d_weights;
+};
+
+// The workgroups behind those of the tokens: one per expert, zeros into its segment's padding.
+template <class T>
+__device__ void clear_padding(const RowsArgs& A) {
+    const int e = (int)(blockIdx.x - A.grid);
+    const int64_t s0 = max((int64_t)A.offsets[e] + A.counts[e], (int64_t)0), s1 = min((int64_t)A.offsets[e + 1], A.rows);
+    Run16<T> zero;
+    zero.fill(0);
+    for (int64_t s = s0; s < s1; ++s)
+        for (int64_t q = blockIdx.y * A.span + threadIdx.x; q < min(A.runs, (blockIdx.y + 1) * A.span); q += kBlock)
+            zero.store(static_cast<typename T::type*>(A.out) + s * A.ld_out, q, A.d);
+}
+
+// f(token, lane in the token's group) for the thread's tokens.  ONE: all lanes of a wave have the same token.
+template <bool ONE, class F>
+__device__ __forceinline__ void each_token(const RowsArgs& A, F f) {
+    int in_group = threadIdx.x / A.lanes;
+    const int lane = threadIdx.x % A.lanes;
+    if (ONE) in_group = __builtin_amdgcn_readfirstlane(in_group);
+    for (int64_t g = blockIdx.x; g < A.token_groups; g += A.grid) {
+        const int64_t i = g * (kBlock / A.lanes) + in_group;
+        if (i < A.n) f(i, lane);
+    }
+}
+
+// rows[slot] = (w) x: a token's run is read once and stored to each of its rows.
+template <class T, bool ONE>
+__global__ __launch_bounds__(kBlock) void k_dispatch(RowsArgs A) {
+    using E = typename T::type;
+    if (blockIdx.x >= A.grid) return clear_padding<T>(A);
+    each_token<ONE>(A, [&](int64_t i, int lane) {
+        const E* x = static_cast<const E*>(A.tokens) + i * A.ld_tokens;
+        const int32_t* slot = A.slot + i * A.k;
+        const int64_t q1 = min(A.runs, (blockIdx.y + 1) * A.span);
+        for (int64_t q = blockIdx.y * A.span + lane; q < q1; q += A.lanes) {
+            Run16<T> v;
+            v.load(x, q, A.d);
+            for (int r = 0; r < A.k; ++r) {
+                const int s = slot[r];
+                if ((uint64_t)(int64_t)s >= (uint64_t)A.rows) continue;
+                E* row = static_cast<E*>(A.out) + s * A.ld_out;
+                if (A.weights) {
+                    const float w = A.weights[i * A.k + r];
+                    float o[Run16<T>::n];
+#pragma unroll
+                    for (int c = 0; c < Run16<T>::n; ++c) o[c] = w * v.at(c);
+                    Run16<T> scaled;
+                    scaled.round(o);
+                    scaled.store(row, q, A.d);
+                } else {
+                    v.store(row, q, A.d);
+                }
+            }
+        }
+    });
+}
+
+constexpr int kAhead = 8;  // rows of a token whose runs are in flight
+
+// y = add + sum_r w_r rows[slot_r], in the order of r, float32, rounded once.
+template <class T, bool ONE>
+__global__ __launch_bounds__(kBlock) void k_combine(RowsArgs A) {
+    using E = typename T::type;
+    constexpr int VE = Run16<T>::n;
+    each_token<ONE>(A, [&](int64_t i, int lane) {
+        const int32_t* slot = A.slot + i * A.k;
+        const int64_t q1 = min(A.runs, (blockIdx.y + 1) * A.span);
+        for (int64_t q = blockIdx.y * A.span + lane; q < q1; q += A.lanes) {
+            float y[VE];
+            Run16<T> v[kAhead];
+            if (A.add) v[0].load(static_cast<const E*>(A.add) + i * A.ld_add, q, A.d);
+#pragma unroll
+            for (int c = 0; c < VE; ++c) y[c] = A.add ? v[0].at(c) : 0.0f;
+            for (int r0 = 0; r0 < A.k; r0 += kAhead) {
+                float w[kAhead];
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r) {
+                    const int s = r0 + r < A.k ? slot[r0 + r] : -1;
+                    const bool in = (uint64_t)(int64_t)s < (uint64_t)A.rows;
+                    w[r] = !in ? 0.0f : A.weights ? A.weights[i * A.k + r0 + r] : 1.0f;
+                    v[r].fill(0);
+                    if (in) v[r].load(static_cast<const E*>(A.in) + s * A.ld_in, q, A.d);
+                }
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r)
+#pragma unroll
+                    for (int c = 0; c < VE; ++c) y[c] = fmaf(w[r], v[r].at(c), y[c]);
+            }
+            v[0].round(y);
+            v[0].store(static_cast<E*>(A.out) + i * A.ld_out, q, A.d);
+        }
+    });
+}
+
+// d_rows[slot_r] = w_r d_y and d_w_r = <rows[slot_r], d_y>: d_y is read once per kAhead rows.  A thread reads a run of
+// a row before it stores the gradient's, so that the gradient may take the rows' place.
+template <class T, int L>
+__global__ __launch_bounds__(kBlock) void k_combine_grad(RowsArgs A) {
+    using E = typename T::type;
+    constexpr int VE = Run16<T>::n, kWaves = L > 64 ? L / 64 : 1;
+    __shared__ float part[kAhead][kWaves];
+    if (blockIdx.x >= A.grid) return clear_padding<T>(A);
+    int in_group = threadIdx.x / L;
+    const int lane = threadIdx.x % L;
+    if (L >= 64) in_group = __builtin_amdgcn_readfirstlane(in_group);
+    for (int64_t g = blockIdx.x; g < A.token_groups; g += A.grid) {
+        const int64_t at = g * (kBlock / L) + in_group, i = min(at, A.n - 1);
+        const bool on = at < A.n;  // (the others repeat the last token and store nothing)
+        const E* dy = static_cast<const E*>(A.tokens) + i * A.ld_tokens;
+        const int32_t* slot = A.slot + i * A.k;
+        for (int r0 = 0; r0 < A.k; r0 += kAhead) {
+            float dot[kAhead], w[kAhead];
+            int64_t s[kAhead];
+#pragma unroll
+            for (int r = 0; r < kAhead; ++r) {
+                const int row = r0 + r < A.k ? slot[r0 + r] : -1;
+                s[r] = (uint64_t)(int64_t)row < (uint64_t)A.rows ? row : -1;
+                w[r] = s[r] < 0 ? 0.0f : A.weights ? A.weights[i * A.k + r0 + r] : 1.0f;
+                dot[r] = 0.0f;
+            }
+            for (int64_t q = lane; q < A.runs; q += L) {
+                Run16<T> dyr, v[kAhead];
+                dyr.load(dy, q, A.d);
+                if (A.d_weights) {
+#pragma unroll
+                    for (int r = 0; r < kAhead; ++r) {
+                        v[r].fill(0);
+                        if (s[r] >= 0) v[r].load(static_cast<const E*>(A.in) + s[r] * A.ld_in, q, A.d);
+                    }
+                }
+                float gf[VE];
+#pragma unroll
+                for (int c = 0; c < VE; ++c) gf[c] = dyr.at(c);
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r) {
+                    if (s[r] < 0) continue;
+                    if (A.d_weights) {
+#pragma unroll
+                        for (int c = 0; c < VE; ++c) dot[r] = fmaf(v[r].at(c), gf[c], dot[r]);
+                    }
+                    if (A.out && on) {
+                        float o[VE];
+#pragma unroll
+                        for (int c = 0; c < VE; ++c) o[c] = w[r] * gf[c];
+                        Run16<T> scaled;
+                        scaled.round(o);
+                        scaled.store(static_cast<E*>(A.out) + s[r] * A.ld_out, q, A.d);
+                    }
+                }
+            }
+            if (!A.d_weights) continue;
+#pragma unroll
+            for (int r = 0; r < kAhead; ++r) dot[r] = lanes_sum<(L < 64 ? L : 64)>(dot[r]);
+            if constexpr (L > 64) {
+                const int wave = threadIdx.x / 64;
+                __syncthreads();
+                if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                    for (int r = 0; r < kAhead; ++r) part[r][wave] = dot[r];
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r) {
+                    dot[r] = 0.0f;
+#pragma unroll
+                    for (int w2 = 0; w2 < kWaves; ++w2) dot[r] += part[r][w2];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kAhead; ++r)
+                if (lane == 0 && on && r0 + r < A.k) A.d_weights[i * A.k + r0 + r] = s[r] < 0 ? 0.0f : dot[r];
+        }
+    }
+}
+
+// ----- host side ------------------------------------------------------------------------
+int lanes_for(int64_t runs, int least) {
+    int lanes = least;
+    while (lanes < kBlock && lanes < runs) lanes *= 2;
+    return lanes;
+}
+
+constexpr int64_t kRowsGrid = 1 << 20;  // workgroups of one launch at most
+
+void share(RowsArgs& A, int lanes) {
+    A.lanes = lanes;
+    const int per = kBlock / lanes;
+    A.token_groups = (A.n + per - 1) / per;
+    A.grid = std::min(A.token_groups, kRowsGrid);
+    A.span = A.runs;
+}
+
+template <class K>
+hipError_t launch_rows(const RowsArgs& A, K kernel, bool pads, hipStream_t s) {
+    const int64_t groups = A.grid + (pads ? A.m : 0);
+    const int64_t parts = (A.runs + A.span - 1) / A.span;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)groups, (unsigned)parts), dim3(kBlock), 0, s, A);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t dispatch(RowsArgs A, hipStream_t s) {
+    A.runs = (A.d + Run16<T>::n - 1) / Run16<T>::n;
+    share(A, lanes_for(A.runs, 8));
+    return launch_rows(A, A.lanes >= 64 ? k_dispatch<T, true> : k_dispatch<T, false>, A.counts != nullptr, s);
+}
+
+template <class T>
+hipError_t combine(RowsArgs A, hipStream_t s) {
+    A.runs = (A.d + Run16<T>::n - 1) / Run16<T>::n;
+    share(A, lanes_for(A.runs, 8));
+    return launch_rows(A, A.lanes >= 64 ? k_combine<T, true> : k_combine<T, false>, false, s);
+}
+
+template <class T>
+hipError_t combine_grad(RowsArgs A, hipStream_t s) {
+    A.runs = (A.d + Run16<T>::n - 1) / Run16<T>::n;
+    share(A, A.runs <= 16 ? 16 : A.runs <= 128 ? 64 : 256);
+    auto kernel = A.lanes == 16 ? k_combine_grad<T, 16> : A.lanes == 64 ? k_combine_grad<T, 64> : k_combine_grad<T, 256>;
+    return launch_rows(A, kernel, A.out && A.counts, s);
+}
+
+// n windows of d elements, stride ld, at address p: what they span in bytes.
+struct Span {
+    uintptr_t lo, hi;
+};
+Span span_of(const void* p, int64_t n, int64_t d, int64_t ld, int es) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, n > 0 ? a + (uintptr_t)(((n - 1) * ld + d) * es) : a};
+}
+bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Sizes shared by the three row operators.
+int check_rows(int32_t dtype, int64_t n, int64_t d, int32_t k, int64_t rows) {
+    if (dtype != SK_F32 && dtype != SK_BF16 && dtype != SK_F16) return SK_ERR_DTYPE;
+    if (n < 0 || n > INT32_MAX || d < 1 || d > INT32_MAX || rows < 0 || rows > INT32_MAX) return SK_ERR_SHAPE;
+    if (k < 1 || k > kRowsMaxTop) return SK_ERR_ROUTE;
+    return SK_OK;
+}
+
+int check_matrix(const void* p, int32_t dtype, int64_t rows, int64_t d, int64_t ld) {
+    if (!good_stride(ld, rows, d)) return SK_ERR_SHAPE;
+    if (rows > 0 && !p) return SK_ERR_NULL;
+    return reinterpret_cast<uintptr_t>(p) % elem_size(dtype) != 0 ? SK_ERR_DTYPE : SK_OK;
+}
+
+// counts and offsets are given together, with m.
+int check_padding(const int32_t* counts, const int32_t* offsets, int64_t m) {
+    if (!counts && !offsets) return SK_OK;
+    if (!counts || !offsets) return SK_ERR_NULL;
+    return m < 1 || m > kRowsMaxExperts ? SK_ERR_SHAPE : SK_OK;
+}
+
+}  // namespace
+}  // namespace sk
+
+using namespace sk;
+
+extern "C" {
+
+int64_t sk_route_sort_rows(int64_t n, int32_t k, int64_t m, int32_t align, int32_t capacity) {
+    return sort_rows(n, k, m, align, capacity);
+}
+
+size_t sk_route_sort_workspace_bytes(int64_t n, int32_t k, int64_t m) {
+    return sort_rows(n, k, m, 1, 0) < 0 ? 0 : sort_plan(n * k, m).total;
+}
+
+int sk_route_sort(const int32_t* idx, int64_t n, int32_t k, int64_t m, int32_t align, int32_t capacity, int32_t* slot,
+                  int32_t* source, int64_t rows, int32_t* counts, int32_t* offsets, void* ws, size_t ws_bytes,
+                  void* stream) {
+    if (n < 0 || n > INT32_MAX || m < 1 || m > kRowsMaxExperts) return SK_ERR_SHAPE;
+    if (k < 1 || k > kRowsMaxTop || align < 1 || capacity < 0) return SK_ERR_ROUTE;
+    const int64_t most = sort_rows(n, k, m, align, capacity);
+    if (most < 0 || rows < most || rows > INT32_MAX) return SK_ERR_SHAPE;
+    if ((n > 0 && (!idx || !slot)) || (rows > 0 && !source) || !counts || !offsets) return SK_ERR_NULL;
+    const SortPlan P = sort_plan(n * k, m);
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < P.total) return SK_ERR_WORKSPACE;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    SortArgs A{};
+    A.idx = idx;
+    A.pairs = n * k;
+    A.rows = rows;
+    A.m = (int)m;
+    while ((m >> A.bits) > 0) ++A.bits;  // the numbers 0 to m
+    A.align = align;
+    A.capacity = capacity;
+    A.per = P.per_thread * kSortThreads;
+    A.groups = P.groups;
+    A.scanned = P.groups > kSortGroups;
+    A.slot = slot;
+    A.source = source;
+    A.counts = counts;
+    A.offsets = offsets;
+    A.hist = static_cast<int32_t*>(ws);
+    if (A.groups > 1) {
+        hipLaunchKernelGGL(k_sort_count, dim3((unsigned)A.groups), dim3(kSortThreads), 0, s, A);
+        SK_TRY_LAUNCH(hipGetLastError());
+    }
+    if (A.scanned) {
+        hipLaunchKernelGGL(k_sort_scan, dim3((unsigned)((m + 63) / 64)), dim3(kSortThreads), 0, s, A);
+        SK_TRY_LAUNCH(hipGetLastError());
+    }
+    SK_TRY_LAUNCH(P.per_thread == 1   ? launch_place<1>(A, s)
+                  : P.per_thread == 2 ? launch_place<2>(A, s)
+                  : P.per_thread == 4 ? launch_place<4>(A, s)
+                  : P.per_thread == 8 ? launch_place<8>(A, s)
+                                      : launch_place<16>(A, s));
+    return SK_OK;
+}
+
+int sk_route_dispatch(const void* x, int32_t dtype, int64_t n, int64_t d, int64_t ld, const int32_t* slot, int32_t k,
+                      const float* weights, const int32_t* counts, const int32_t* offsets, int64_t m, void* out,
+                      int64_t rows, int64_t ld_out, void* stream) {
+    int st = check_rows(dtype, n, d, k, rows);
+    if (st) return st;
+    if ((st = check_matrix(x, dtype, n, d, ld)) || (st = check_matrix(out, dtype, rows, d, ld_out))) return st;
+    if ((st = check_padding(counts, offsets, m))) return st;
+    if (n == 0 || rows == 0) return SK_OK;
+    if (!slot) return SK_ERR_NULL;
+    if (meet(span_of(x, n, d, ld, elem_size(dtype)), span_of(out, rows, d, ld_out, elem_size(dtype)))) return SK_ERR_OVERLAP;
+    RowsArgs A{};
+    A.n = n;
+    A.d = d;
+    A.rows = rows;
+    A.k = k;
+    A.m = (int)m;
+    A.slot = slot;
+    A.counts = counts;
+    A.offsets = offsets;
+    A.weights = weights;
+    A.tokens = x;
+    A.ld_tokens = ld;
+    A.out = out;
+    A.ld_out = ld_out;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    SK_TRY_LAUNCH(dtype == SK_F32 ? dispatch<F32>(A, s) : dtype == SK_BF16 ? dispatch<Bf16>(A, s) : dispatch<F16>(A, s));
+    return SK_OK;
+}
+
+int sk_route_combine(const void* in, int32_t dtype, int64_t rows, int64_t d, int64_t ld_in, const int32_t* slot,
+                     int64_t n, int32_t k, const float* weights, const void* add, int64_t ld_add, void* y, int64_t ld_y,
+                     void* stream) {
+    int st = check_rows(dtype, n, d, k, rows);
+    if (st) return st;
+    if ((st = check_matrix(in, dtype, rows, d, ld_in)) || (st = check_matrix(y, dtype, n, d, ld_y))) return st;
+    if (add && (st = check_matrix(add, dtype, n, d, ld_add))) return st;
+    if (n == 0) return SK_OK;
+    if (!slot) return SK_ERR_NULL;
+    const int es = elem_size(dtype);
+    const Span out = span_of(y, n, d, ld_y, es);
+    if (meet(span_of(in, rows, d, ld_in, es), out)) return SK_ERR_OVERLAP;
+    const bool in_place = add == y && (ld_add == ld_y || n == 1);
+    if (add && !in_place && meet(span_of(add, n, d, ld_add, es), out)) return SK_ERR_OVERLAP;
+    RowsArgs A{};
+    A.n = n;
+    A.d = d;
+    A.rows = rows;
+    A.k = k;
+    A.slot = slot;
+    A.weights = weights;
+    A.add = add;
+    A.ld_add = ld_add;
+    A.in = in;
+    A.ld_in = ld_in;
+    A.out = y;
+    A.ld_out = ld_y;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    SK_TRY_LAUNCH(dtype == SK_F32 ? combine<F32>(A, s) : dtype == SK_BF16 ? combine<Bf16>(A, s) : combine<F16>(A, s));
+    return SK_OK;
+}
+
+int sk_route_combine_grad(const void* in, int32_t dtype, int64_t rows, int64_t d, int64_t ld_in, const int32_t* slot,
+                          int64_t n, int32_t k, const float* weights, const int32_t* counts, const int32_t* offsets,
+                          int64_t m, const void* d_y, int64_t ld_dy, void* d_rows, int64_t ld_out, float* d_weights,
+                          void* stream) {
+    int st = check_rows(dtype, n, d, k, rows);
+    if (st) return st;
+    if (d_weights && (st = check_matrix(in, dtype, rows, d, ld_in))) return st;
+    if ((st = check_matrix(d_y, dtype, n, d, ld_dy))) return st;
+    if (d_rows && (st = check_matrix(d_rows, dtype, rows, d, ld_out))) return st;
+    if ((st = check_padding(counts, offsets, m))) return st;
+    if (n == 0) return SK_OK;
+    if (!slot || (!d_rows && !d_weights)) return SK_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (d_rows) {
+        const Span out = span_of(d_rows, rows, d, ld_out, es);
+        if (meet(span_of(d_y, n, d, ld_dy, es), out)) return SK_ERR_OVERLAP;
+        const bool in_place = in == d_rows && (ld_in == ld_out || rows == 1);
+        if (d_weights && !in_place && meet(span_of(in, rows, d, ld_in, es), out)) return SK_ERR_OVERLAP;
+    }
+    RowsArgs A{};
+    A.n = n;
+    A.d = d;
+    A.rows = rows;
+    A.k = k;
+    A.m = (int)m;
+    A.slot = slot;
+    A.counts = counts;
+    A.offsets = offsets;
+    A.weights = weights;
+    A.tokens = d_y;
+    A.ld_tokens = ld_dy;
+    A.in = in;
+    A.ld_in = ld_in;
+    A.out = rows > 0 ? d_rows : nullptr;
+    A.ld_out = ld_out;
+    A.d_weights = d_weights;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    SK_TRY_LAUNCH(dtype == SK_F32 ? combine_grad<F32>(A, s) : dtype == SK_BF16 ? combine_grad<Bf16>(A, s) : combine_grad<F16>(A, s));
+    return SK_OK;
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
 // sk_scores.hpp -- what the operators on a given score matrix share
-// (sk_scores_solve.hip, sk_scores_route.hip, sk_scores_logprobs.hip): element
+// (sk_scores_solve.hip, sk_scores_route.hip, sk_scores_logprobs.hip,
+// sk_scores_verify.hip) and on rows of tokens (sk_route_rows.hip): element
 // types, reductions inside a wave without LDS, argument checks.
 //
 // A score matrix is row-major, n rows of m scores with a row stride of ld
@@ -203,6 +204,55 @@ struct Row {
     // Whether the rows of a matrix can be read and written in runs.
     static bool fits(const void* p, int64_t ld, int64_t m) {
         return W > 1 && m % W == 0 && ld % W == 0 && reinterpret_cast<uintptr_t>(p) % (W * sizeof(Elem)) == 0;
+    }
+};
+
+// ----- 16 bytes of a row, at any address of its element type ------------------------------
+// Such loads and stores need no alignment on this GPU, so rows of odd length or at odd addresses go the same way.
+template <class T>
+struct Run16 {
+    using Elem = typename T::type;
+    static constexpr int n = 16 / (int)sizeof(Elem);
+    uint4 raw;
+    __device__ __forceinline__ uint32_t word(int w) const { return w == 0 ? raw.x : w == 1 ? raw.y : w == 2 ? raw.z : raw.w; }
+    __device__ __forceinline__ Elem bits(int i) const {
+        if constexpr (n == 4)
+            return __builtin_bit_cast(float, word(i));
+        else
+            return (uint16_t)(i % 2 ? word(i / 2) >> 16 : word(i / 2) & 0xffffu);
+    }
+    __device__ __forceinline__ float at(int i) const { return T::to(bits(i)); }
+    __device__ __forceinline__ void set(const Elem (&v)[n]) { __builtin_memcpy(&raw, v, 16); }
+    __device__ __forceinline__ void round(const float (&v)[n]) {
+        Elem e[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) e[i] = T::from(v[i]);
+        set(e);
+    }
+    __device__ __forceinline__ void fill(uint32_t w) { raw = make_uint4(w, w, w, w); }
+    __device__ __forceinline__ void get(const Elem* p) { __builtin_memcpy(&raw, p, 16); }
+    __device__ __forceinline__ void put(Elem* p) const { __builtin_memcpy(p, &raw, 16); }
+    // Run q of a row of d elements: behind the row's end the elements read as 0 and are not written.
+    __device__ __forceinline__ void load(const Elem* row, int64_t q, int64_t d) {
+        const int64_t j = q * n;
+        if (j + n <= d) {
+            get(row + j);
+        } else {
+            Elem v[n];
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] = j + i < d ? row[j + i] : Elem(0);
+            set(v);
+        }
+    }
+    __device__ __forceinline__ void store(Elem* row, int64_t q, int64_t d) const {
+        const int64_t j = q * n;
+        if (j + n <= d) {
+            put(row + j);
+        } else {
+#pragma unroll
+            for (int i = 0; i < n - 1; ++i)
+                if (j + i < d) row[j + i] = bits(i);
+        }
     }
 };
 

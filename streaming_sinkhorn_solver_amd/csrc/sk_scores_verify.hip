@@ -1,0 +1,719 @@
+// sk_scores_verify.hip -- drafted tokens against the target's probabilities
+// (sk_scores_verify).
+//
+// With p = softmax(s / eps) of the target's row and q = softmax(t / eps_draft) of
+// the draft's, or q one at the drafted token, a token x drawn from q is taken if
+// u q(x) < p(x); in its place, at the first row where it is not, comes a draw from
+// the residual max(p - q, 0).  That pair of draws is the maximal coupling of q and
+// p, the transport plan of least cost 1[x != y].
+//
+// A decision or a draw next to a border must not depend on how sums are taken, so
+// exponentials and sums are in float64 throughout (a float64 FMA issues as fast as
+// a float32 one here): the error of a probability is some 2^-49 of it, where a row of
+// 131072 has borders 2^-20 apart and the random numbers are multiples of 2^-24.
+#include "sk_scores.hpp"
+
+#include <algorithm>
+
+namespace sk {
+namespace {
+
+constexpr int64_t kVfGrid = 1 << 20;  // workgroups of one launch (each may serve several rows)
+constexpr int64_t kVfMaxCols = (int64_t)1 << 30;
+constexpr int kVfVecs = 4;            // 16-byte loads of a thread's block
+constexpr int kVfChunk = 2048;        // entries of the residual whose sum is kept
+constexpr int kVfFill = 1024, kVfCutMin = 1024;
+constexpr double kFloor = -1000.0;    // exponents below count as zero
+constexpr double kUnset = -1.0e300;   // reference of a part without an unmasked entry
+
+// What is needed of a row, or a part of one: sum of 2^(c (s - ref)); NaN if a score is NaN or +inf.  The reference is a
+// score, and the difference to it is taken first: rows of a type's lowest value lose nothing.
+struct Sum {
+    double ref, s;
+};
+
+// What a request's draw needs.
+struct Draw {
+    double ref_p, log_p;  // reference of the row's sum, and the sum's log2
+    double ref_q, log_q;  // of the draft's row
+    int64_t row;          // where the request stops, -1: nothing is drawn
+    int64_t out;          // column that the residual leaves out, or -1
+    int64_t with_q;
+};
+
+struct VfArgs {
+    const void *s, *q;
+    int64_t ld, ldq, n, b;
+    int m;
+    double c, cq;  // log2e / eps
+    const int64_t *tokens, *starts;
+    const float *u_accept, *u_sample;
+    int32_t* accepted;
+    int64_t *next, *out_tokens;
+    float *ratio, *logp;
+    int splits, cut;  // parts of a row, and the runs of 16 bytes of one
+    int chunks, parts;
+    Sum* sums;        // [n][2][splits]
+    double* chunk;    // [b][chunks]
+    Draw* draw;       // [b]
+};
+
+// 2^(d c) for d c in [kFloor, 1000]: the exponent is k + f with |f| <= 1/2, 2^f by the polynomial that meets it at the
+// ten Chebyshev points and at 0 (within 2^-50.6), k added to the exponent.  2^0 is 1 exactly.
+__device__ __forceinline__ double pow2(double d, double c) {
+    constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52: the sum's low word is the nearest integer
+    const double t = fma(d, c, kRound);
+    const double f = fma(d, c, -(t - kRound));
+    double p = 0x1.e5e9f548e5725p-28;
+    p = fma(p, f, 0x1.b6571de2f2351p-24);
+    p = fma(p, f, 0x1.62bfe46117445p-20);
+    p = fma(p, f, 0x1.ffcb76789860fp-17);
+    p = fma(p, f, 0x1.4309130378460p-13);
+    p = fma(p, f, 0x1.5d87fe908f88ap-10);
+    p = fma(p, f, 0x1.3b2ab6fba385fp-7);
+    p = fma(p, f, 0x1.c6b08d7044119p-5);
+    p = fma(p, f, 0x1.ebfbdff82c590p-3);
+    p = fma(p, f, 0x1.62e42fefa39f7p-1);
+    p = fma(p, f, 1.0);
+    const uint64_t bits = __builtin_bit_cast(uint64_t, p);
+    const uint32_t k = (uint32_t)__builtin_bit_cast(uint64_t, t);
+    return __builtin_bit_cast(double, bits + ((uint64_t)k << 52));
+}
+// 2^y; 0 below the floor (a masked score's exponent is -inf).
+__device__ __forceinline__ double pow2_or_zero(double y) {
+    const double v = pow2(fmax(y, kFloor), 1.0);
+    return y > kFloor ? v : 0.0;
+}
+
+// A sum taken to another, no lower reference; an unset one is 0 there.
+__device__ __forceinline__ double moved(Sum a, double ref, double c) {
+    return a.ref == ref ? a.s : a.s * pow2_or_zero((a.ref - ref) * c);
+}
+__device__ __forceinline__ Sum join(Sum a, Sum b, double c) {
+    const double ref = fmax(a.ref, b.ref);
+    return {ref, moved(a, ref, c) + moved(b, ref, c)};
+}
+template <int L>
+__device__ __forceinline__ Sum lanes_join(Sum a, double c) {
+    double ref = a.ref;
+    for (int o = 1; o < L; o *= 2) ref = fmax(ref, __shfl_xor(ref, o));
+    return {ref, lanes_sum<L>(moved(a, ref, c))};
+}
+
+// Whether row i of the target is one that a request looks at.  All lanes of a wave, i the same in each.
+__device__ bool row_counts(const VfArgs& A, int64_t i, int lane) {
+    if (i < A.starts[0] || i >= A.starts[A.b]) return false;
+    if (i > 0 && A.tokens[i - 1] >= 0) return true;
+    // behind a row without a drafted token only a request's first row counts: a search by 64 at a time
+    int64_t lo = 0, size = A.b;
+    while (size > 64) {
+        const int64_t step = (size + 63) / 64, at = lo + lane * step;
+        const uint64_t mask = __ballot(at < lo + size && A.starts[min(at, A.b)] <= i);
+        const int below = __popcll(mask);
+        if (below == 0) return false;
+        const int64_t end = lo + size;
+        lo += (int64_t)(below - 1) * step;
+        size = min(step, end - lo);
+    }
+    return __ballot(lane < size && A.starts[min(lo + lane, A.b)] == i) != 0;
+}
+
+// Sums of the rows' exponentials: a row, or a part of one, per W waves.
+template <class T, int W>
+__global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A, int kinds) {
+    using E = typename T::type;
+    constexpr int VE = Run16<T>::n, kThreads = W * 64, kRows = kBlock / kThreads, NV = kVfVecs, kStep = kThreads * NV;
+    __shared__ Sum red[kBlock / 64];
+    const int t = threadIdx.x % kThreads, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    const int64_t items = A.n * A.splits * kinds;
+    for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items; item0 += (int64_t)gridDim.x * kRows) {
+        const int64_t item = item0 + slot;
+        if (item >= items) return;  // (one wave per row: no barrier below)
+        const int64_t i = item / (A.splits * kinds);
+        const int kind = (int)(item / A.splits % kinds), split = (int)(item % A.splits);
+        const bool draft = kind == 1;
+        if ((draft && A.tokens[i] < 0) || !row_counts(A, i, lane)) continue;
+        const E* row = static_cast<const E*>(draft ? A.q : A.s) + i * (draft ? A.ldq : A.ld);
+        const double c = draft ? A.cq : A.c;
+        const int runs = A.m / VE, tail = A.m - runs * VE;
+        const int v0 = split * A.cut, v1 = min(runs, v0 + A.cut);
+        const int blocks = v1 > v0 ? (v1 - v0 + kStep - 1) / kStep : 0;
+        Run16<T> next[NV], v[NV];
+        auto fetch = [&](int b) {
+#pragma unroll
+            for (int q = 0; q < NV; ++q) next[q].get(row + (int64_t)min(v0 + b * kStep + q * kThreads + t, v1 - 1) * VE);
+        };
+        if (blocks > 0) fetch(0);
+        double ref = 0.0, S = 0.0;
+        const double floor = kFloor / c;
+        float limit = -INFINITY;  // a larger score moves the reference
+        bool set = false, bad = false;
+        auto raise = [&](float top) {
+            if (!(top < INFINITY)) bad = true;  // NaN or +inf
+            if (!(top > limit) || bad) return;
+            S = set ? moved({ref, S}, top, c) : 0.0;
+            ref = top;
+            limit = (float)(ref + 400.0 / c);
+            set = true;
+        };
+        if (split == 0 && t < tail) {
+            const float x = T::to(row[runs * VE + t]);
+            raise(x);
+            if (set) S += pow2_or_zero(((double)x - ref) * c);
+        }
+        for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+            for (int q = 0; q < NV; ++q) v[q] = next[q];
+            if (b + 1 < blocks) {
+                fetch(b + 1);
+            } else {
+#pragma unroll
+                for (int q = 0; q < NV; ++q)
+                    if (v0 + b * kStep + q * kThreads + t >= v1)
+                        v[q].fill(T::kNegInfBits);
+            }
+            float top = v[0].at(0);
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) top = __builtin_elementwise_maximum(top, v[q].at(e));  // (keeps a NaN)
+            raise(top);
+            double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+#pragma unroll
+                for (int e = 0; e < VE; e += 2) {
+                    // (a masked score's 2^-1000 is lost against the 1 of the reference)
+                    s0 += pow2(fmax((double)v[q].at(e) - ref, floor), c);
+                    s1 += pow2(fmax((double)v[q].at(e + 1) - ref, floor), c);
+                }
+            S += s0 + s1;
+        }
+        Sum sum{set ? ref : kUnset, bad ? (double)NAN : set ? S : 0.0};
+        sum = lanes_join<64>(sum, c);
+        if (W > 1) {
+            __syncthreads();
+            if (lane == 0) red[wave] = sum;
+            __syncthreads();
+            sum = red[0];
+#pragma unroll
+            for (int w = 1; w < W; ++w) sum = join(sum, red[w], c);
+        }
+        if (t == 0) A.sums[(i * 2 + kind) * A.splits + split] = sum;
+    }
+}
+
+// A row's reference and the log2 of its sum; log2 of a column's probability.
+struct RowLog {
+    double ref, log_sum;  // -inf: no unmasked entry; NaN: a NaN or +inf score
+};
+__device__ __forceinline__ RowLog row_log(const VfArgs& A, int64_t i, int kind) {
+    const Sum* p = A.sums + (i * 2 + kind) * A.splits;
+    Sum sum = p[0];
+    for (int k = 1; k < A.splits; ++k) sum = join(sum, p[k], kind ? A.cq : A.c);
+    return {sum.ref, sum.s == 0.0 ? -(double)INFINITY : log2(sum.s)};
+}
+template <class T>
+__device__ __forceinline__ double column_log(const void* m, int64_t ld, int64_t i, int64_t j, double c, const RowLog& r) {
+    const float s = T::to(static_cast<const typename T::type*>(m)[i * ld + j]);
+    if (r.log_sum != r.log_sum) return r.log_sum;
+    return s == -INFINITY ? -(double)INFINITY : fma((double)s - r.ref, c, -r.log_sum);
+}
+
+// p(x) / q(x) of row i's drafted token x, at most 1; NaN where one of the rows holds a NaN or +inf.
+template <class T>
+__device__ __forceinline__ double ratio_of(const VfArgs& A, int64_t i, int64_t token, const RowLog& p, const RowLog& q) {
+    const bool in = token < A.m;  // a token that the vocabulary does not have: p is 0
+    const double lp = in ? column_log<T>(A.s, A.ld, i, token, A.c, p) : -(double)INFINITY;
+    const double lq = !A.q ? 0.0 : in ? column_log<T>(A.q, A.ldq, i, token, A.cq, q) : q.log_sum;
+    if (p.log_sum != p.log_sum || lq != lq) return (double)NAN;
+    if (lp < kFloor) return 0.0;
+    const double d = lp - lq;
+    return d >= 0.0 || lq < kFloor ? 1.0 : exp2(d);
+}
+
+struct Rows {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ Rows rows_of(const VfArgs& A, int64_t r) {
+    const int64_t lo = min(max(A.starts[r], (int64_t)0), A.n), hi = min(max(A.starts[r + 1], lo), A.n);
+    return {lo, hi};
+}
+
+// Where a request stops, by all lanes of a wave: the first row whose token is not taken or that has none.
+template <class T>
+__device__ Draw stop_of(const VfArgs& A, int64_t r, int lane) {
+    Draw d{0.0, 0.0, 0.0, 0.0, -1, -1, 0};
+    const Rows R = rows_of(A, r);
+    for (int64_t i0 = R.lo; i0 < R.hi; i0 += 64) {
+        const int64_t i = i0 + lane;
+        int64_t token = -1;
+        RowLog p{0.0, 0.0}, q{0.0, 0.0};
+        bool stop = false;
+        if (i < R.hi) {
+            // rows behind one without a drafted token have no sums; they lie behind the stop
+            token = A.tokens[i];
+            p = row_log(A, i, 0);
+            if (A.q && token >= 0) q = row_log(A, i, 1);
+            if (token >= 0) {
+                const double ratio = ratio_of<T>(A, i, token, p, q);
+                stop = !((double)A.u_accept[i] < ratio && ratio > 0.0);
+            } else {
+                stop = true;
+            }
+        }
+        const uint64_t mask = __ballot(stop);
+        if (!mask) continue;
+        const int at = __ffsll((unsigned long long)mask) - 1;
+        d.row = i0 + at;
+        d.ref_p = __shfl(p.ref, at);
+        d.ref_q = __shfl(q.ref, at);
+        d.log_p = __shfl(p.log_sum, at);
+        d.log_q = __shfl(q.log_sum, at);
+        token = __shfl((long long)token, at);
+        d.with_q = A.q && token >= 0;
+        d.out = !A.q && token >= 0 && token < A.m ? token : -1;
+        break;
+    }
+    return d;
+}
+
+// An entry of what is drawn from: max(p - q, 0), or, where no draft scores take part, p relative to its reference.
+template <class T>
+__device__ __forceinline__ double weight(const VfArgs& A, const Draw& d, float s, float t, int64_t j) {
+    if (d.with_q) {
+        const double p = pow2_or_zero(fma((double)s - d.ref_p, A.c, -d.log_p));
+        const double q = t == -INFINITY ? 0.0 : pow2_or_zero(fma((double)t - d.ref_q, A.cq, -d.log_q));
+        return fmax(p - q, 0.0);
+    }
+    return j == d.out ? 0.0 : pow2_or_zero(((double)s - d.ref_p) * A.c);
+}
+__device__ __forceinline__ bool drawable(const Draw& d) {
+    const bool p = d.log_p > -(double)INFINITY;  // (NaN: no)
+    return d.row >= 0 && p && (!d.with_q || d.log_q == d.log_q);
+}
+
+// Sum of a chunk's weights, by all lanes of a wave, the same in each.
+template <class T>
+__device__ __forceinline__ double chunk_sum(const VfArgs& A, const Draw& d, int chunk, int lane) {
+    using E = typename T::type;
+    constexpr int VE = Run16<T>::n, NV = kVfChunk / 64 / VE;
+    const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
+    const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
+    const int j0 = chunk * kVfChunk;
+    double sum = 0.0;
+    if (A.m - j0 >= kVfChunk) {
+        Run16<T> a[NV], b[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            a[v].get(s + j0 + (v * 64 + lane) * VE);
+            b[v].get(q + j0 + (v * 64 + lane) * VE);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sum += weight<T>(A, d, a[v].at(e), b[v].at(e), j0 + (v * 64 + lane) * VE + e);
+    } else {
+        for (int64_t j = j0 + lane; j < A.m; j += 64) sum += weight<T>(A, d, T::to(s[j]), T::to(q[j]), j);
+    }
+    return lanes_sum<64>(sum);
+}
+
+// Sums of the chunks of what each request draws from: a wave per chunk, A.parts workgroups per request.
+template <class T>
+__global__ __launch_bounds__(kBlock) void k_verify_chunks(VfArgs A) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    for (int64_t item = blockIdx.x; item < A.b * A.parts; item += gridDim.x) {
+        const int64_t r = item / A.parts;
+        const int part = (int)(item % A.parts);
+        const Draw d = stop_of<T>(A, r, lane);
+        if (part == 0 && threadIdx.x == 0) A.draw[r] = d;
+        if (!drawable(d)) continue;
+        for (int k = part * (kBlock / 64) + wave; k < A.chunks; k += A.parts * (kBlock / 64)) {
+            const double sum = chunk_sum<T>(A, d, k, lane);
+            if (lane == 0) A.chunk[r * A.chunks + k] = sum;
+        }
+    }
+}
+
+// Inclusive sums over the workgroup's threads; the last is the same in every thread.
+__device__ __forceinline__ double block_scan(double x, double* lds, double& total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    for (int o = 1; o < 64; o *= 2) {
+        const double low = __shfl_up(x, o);
+        if (lane >= o) x += low;
+    }
+    __syncthreads();
+    if (lane == 63) lds[wave] = x;
+    __syncthreads();
+    double before = 0.0;
+    total = 0.0;
+#pragma unroll
+    for (int w = 0; w < kBlock / 64; ++w) {
+        if (w == wave) before = total;
+        total += lds[w];
+    }
+    return before + x;
+}
+
+// The draw and a request's outputs: one workgroup per request.
+template <class T>
+__global__ __launch_bounds__(kBlock) void k_verify_draw(VfArgs A) {
+    using E = typename T::type;
+    __shared__ double lds[kBlock / 64];
+    __shared__ int found, last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    constexpr int kPer = kVfChunk / kBlock;
+    for (int64_t r = blockIdx.x; r < A.b; r += gridDim.x) {
+        Draw d = A.draw[r];
+        const Rows R = rows_of(A, r);
+        int64_t token = -1;
+        if (drawable(d)) {
+            double* chunk = A.chunk + r * A.chunks;
+            double total = 0.0;
+            for (int pass = 0; pass < 2; ++pass) {
+                total = 0.0;
+                for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
+                    double here;
+                    block_scan(k0 + tid < A.chunks ? chunk[k0 + tid] : 0.0, lds, here);
+                    total += here;
+                }
+                if (total > 0.0 || pass == 1) break;
+                // nothing is left of p (q holds all of it): the draw is from p itself
+                d.with_q = 0;
+                d.out = -1;
+                __syncthreads();
+                for (int k = wave; k < A.chunks; k += kBlock / 64) {
+                    const double sum = chunk_sum<T>(A, d, k, lane);
+                    if (lane == 0) chunk[k] = sum;
+                }
+                __syncthreads();
+            }
+            if (total > 0.0) {
+                const double mark = (double)fminf(fmaxf(A.u_sample[r], 0.0f), 1.0f) * total;
+                // the first chunk whose sum with those before exceeds the mark (at the end: the last that has a sum)
+                if (tid == 0) found = INT_MAX, last = -1;
+                double before = 0.0;
+                for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
+                    const int k = k0 + tid;
+                    const double mine = k < A.chunks ? chunk[k] : 0.0;
+                    double here;
+                    const double upto = before + block_scan(mine, lds, here);
+                    if (mine > 0.0) {
+                        atomicMax(&last, k);
+                        if (upto > mark) atomicMin(&found, k);
+                    }
+                    before += here;
+                    __syncthreads();
+                    if (found != INT_MAX) break;
+                }
+                __syncthreads();
+                const int at = found != INT_MAX ? found : last;
+                // the sum before it, in the same order
+                double prior = 0.0;
+                for (int k0 = 0; k0 <= at; k0 += kBlock) {
+                    double here;
+                    block_scan(k0 + tid < at ? chunk[k0 + tid] : 0.0, lds, here);
+                    prior += here;
+                }
+                __syncthreads();
+                if (tid == 0) found = INT_MAX, last = -1;
+                const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
+                const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
+                const int j0 = at * kVfChunk + tid * kPer;
+                double w[kPer], mine = 0.0;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    const int j = j0 + e;
+                    w[e] = j < A.m ? weight<T>(A, d, T::to(s[j]), T::to(q[j]), j) : 0.0;
+                    mine += w[e];
+                }
+                double here;
+                double run = prior + (block_scan(mine, lds, here) - mine);
+                int first = INT_MAX, possible = -1;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    run += w[e];
+                    if (w[e] > 0.0) {
+                        possible = j0 + e;
+                        if (run > mark && first == INT_MAX) first = j0 + e;
+                    }
+                }
+                if (possible >= 0) atomicMax(&last, possible);
+                if (first != INT_MAX) atomicMin(&found, first);
+                __syncthreads();
+                token = found != INT_MAX ? found : last;  // (roundings: the last possible entry of the chunk)
+            }
+        }
+        const int64_t stop = d.row >= 0 ? d.row : R.hi;
+        bool ended = false;
+        for (int64_t i0 = R.lo; i0 < R.hi; i0 += kBlock) {
+            const int64_t i = i0 + tid;
+            // rows behind one without a drafted token take no part
+            const int64_t drafted = i < R.hi ? A.tokens[i] : 0;
+            const bool none = i < R.hi && drafted < 0;
+            const uint64_t mask = __ballot(none);
+            __syncthreads();
+            if (tid == 0) found = INT_MAX;
+            __syncthreads();
+            if (mask && lane == 0) atomicMin(&found, wave * 64 + __ffsll((unsigned long long)mask) - 1);
+            __syncthreads();
+            const int first_none = found;
+            if (i < R.hi) {
+                const bool in = !ended && tid <= first_none;
+                const int64_t emitted = i < stop ? drafted : i == stop ? token : -1;
+                float ratio = 0.0f, logp = 0.0f;
+                if (in) {
+                    const RowLog p = row_log(A, i, 0);
+                    if (!none) {
+                        RowLog q{0.0, 0.0};
+                        if (A.q) q = row_log(A, i, 1);
+                        ratio = (float)ratio_of<T>(A, i, drafted, p, q);
+                    }
+                    if (emitted >= 0)
+                        logp = (float)(column_log<T>(A.s, A.ld, i, emitted, A.c, p) * 0.6931471805599453094);
+                }
+                A.out_tokens[i] = emitted;
+                A.ratio[i] = ratio;
+                A.logp[i] = logp;
+            }
+            ended = ended || first_none != INT_MAX;
+        }
+        if (tid == 0) {
+            A.accepted[r] = (int32_t)(stop - R.lo);
+            A.next[r] = token;
+        }
+        __syncthreads();
+    }
+}
+
+// ----- greedy: p is one at the row's largest score, the first of equal ones -----------------
+// Part: (ordered score, ~column) of the largest entry; 0: no unmasked entry; all ones: a NaN or +inf score.
+template <class T, int W>
+__global__ __launch_bounds__(kBlock) void k_verify_best(VfArgs A) {
+    using E = typename T::type;
+    constexpr int VE = Run16<T>::n, kThreads = W * 64, kRows = kBlock / kThreads, NV = kVfVecs, kStep = kThreads * NV;
+    __shared__ uint64_t red[kBlock / 64];
+    const int t = threadIdx.x % kThreads, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    uint64_t* best_of = reinterpret_cast<uint64_t*>(A.sums);
+    const int64_t items = A.n * A.splits;
+    for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items; item0 += (int64_t)gridDim.x * kRows) {
+        const int64_t item = item0 + slot;
+        if (item >= items) return;
+        const int64_t i = item / A.splits;
+        const int split = (int)(item % A.splits);
+        if (!row_counts(A, i, lane)) continue;
+        const E* row = static_cast<const E*>(A.s) + i * A.ld;
+        const int runs = A.m / VE, tail = A.m - runs * VE;
+        const int v0 = split * A.cut, v1 = min(runs, v0 + A.cut);
+        float best = -INFINITY;
+        int at = -1;  // run of the largest; its entries are looked at again below
+        auto see = [&](float top, int v) {
+            // a NaN takes the lead and keeps it
+            if (!(top <= best) && best == best) best = top, at = v;
+        };
+        for (int b = v0 + t; b < v1; b += kStep) {
+            Run16<T> v[NV];
+#pragma unroll
+            for (int q = 0; q < NV; ++q) v[q].get(row + (int64_t)min(b + q * kThreads, v1 - 1) * VE);
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                float top = v[q].at(0);
+#pragma unroll
+                for (int e = 1; e < VE; ++e) top = __builtin_elementwise_maximum(top, v[q].at(e));
+                see(top, min(b + q * kThreads, v1 - 1));
+            }
+        }
+        int column = at * VE;
+        if (at >= 0) {
+            Run16<T> v;
+            v.get(row + (int64_t)at * VE);
+#pragma unroll
+            for (int e = VE - 1; e >= 0; --e)
+                if (v.at(e) == best) column = at * VE + e;
+        }
+        if (split == 0 && t < tail) {
+            const float x = T::to(row[runs * VE + t]);
+            see(x, runs);
+            if (at == runs) column = runs * VE + t;
+        }
+        uint64_t key = at < 0 ? 0 : !(best < INFINITY) ? ~0ull : (uint64_t)ordered(best) << 32 | (uint32_t)~column;
+        for (int o = 1; o < 64; o *= 2) {
+            const uint64_t other = (uint64_t)__shfl_xor((unsigned long long)key, o);
+            key = key > other ? key : other;
+        }
+        if (W > 1) {
+            __syncthreads();
+            if (lane == 0) red[wave] = key;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < W; ++w) key = key > red[w] ? key : red[w];
+        }
+        if (t == 0) best_of[i * A.splits + split] = key;
+    }
+}
+
+// A wave per request.
+__global__ __launch_bounds__(kBlock) void k_verify_greedy(VfArgs A) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t* best_of = reinterpret_cast<const uint64_t*>(A.sums);
+    for (int64_t r = (int64_t)blockIdx.x * (kBlock / 64) + threadIdx.x / 64; r < A.b; r += (int64_t)gridDim.x * (kBlock / 64)) {
+        const Rows R = rows_of(A, r);
+        int64_t stop = -1, token = -1;
+        bool ended = false;
+        for (int64_t i0 = R.lo; i0 < R.hi; i0 += 64) {
+            const int64_t i = i0 + lane;
+            const bool on = i < R.hi;
+            const int64_t drafted = on ? A.tokens[i] : 0;
+            const uint64_t none = __ballot(on && drafted < 0);
+            const int first_none = none ? __ffsll((unsigned long long)none) - 1 : 64;
+            const bool in = on && !ended && lane <= first_none;
+            uint64_t key = 0;
+            if (in)
+                for (int k = 0; k < A.splits; ++k) key = max(key, best_of[i * A.splits + k]);
+            const bool bad = key == ~0ull;
+            const int64_t best = key == 0 || bad ? -1 : (int64_t)(uint32_t)~(uint32_t)key;
+            const bool hit = drafted >= 0 && drafted == best;
+            if (stop < 0) {
+                const uint64_t mask = __ballot(in && !hit);
+                if (mask) {
+                    const int at = __ffsll((unsigned long long)mask) - 1;
+                    stop = i0 + at;
+                    token = __shfl((long long)best, at);
+                }
+            }
+            if (on) {
+                A.out_tokens[i] = ended ? -1 : stop < 0 || i < stop ? drafted : i == stop ? token : -1;
+                A.ratio[i] = !in || drafted < 0 ? 0.0f : bad ? NAN : hit ? 1.0f : 0.0f;
+                A.logp[i] = 0.0f;
+            }
+            ended = ended || none != 0;
+        }
+        if (lane == 0) {
+            A.accepted[r] = (int32_t)((stop < 0 ? R.hi : stop) - R.lo);
+            A.next[r] = token;
+        }
+    }
+}
+
+// ----- host side ------------------------------------------------------------------------
+struct VfPlan {
+    int splits, cut, chunks, parts;
+    size_t sums, chunk, draw, total;
+};
+
+VfPlan vf_plan(int es, int64_t n, int64_t m, int64_t b) {
+    VfPlan P{};
+    const int64_t runs = std::max<int64_t>(1, m * es / 16);
+    const int64_t most = std::max<int64_t>(1, std::min((kVfFill + n - 1) / std::max<int64_t>(n, 1), runs / kVfCutMin));
+    const int64_t cut = (runs + most - 1) / most;
+    P.cut = (int)cut;
+    P.splits = (int)((runs + cut - 1) / cut);
+    P.chunks = (int)((m + kVfChunk - 1) / kVfChunk);
+    const int64_t whole = (P.chunks + 3) / 4;
+    P.parts = (int)std::max<int64_t>(1, std::min<int64_t>(whole, (kVfFill + b - 1) / std::max<int64_t>(b, 1)));
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    P.chunk = up((size_t)n * 2 * (size_t)P.splits * sizeof(Sum));
+    P.draw = P.chunk + up((size_t)b * (size_t)P.chunks * sizeof(double));
+    P.total = P.draw + up((size_t)b * sizeof(Draw)) + 256;
+    return P;
+}
+
+template <class T>
+hipError_t verify(const VfArgs& A, bool greedy, hipStream_t s) {
+    const bool wave = A.m / Run16<T>::n <= 2 * 64 * kVfVecs;  // such a row, of two blocks at most, is one wave's
+    const int kinds = A.q && !greedy ? 2 : 1, rows = wave ? kBlock / 64 : 1;
+    const int64_t items = A.n * A.splits * kinds;
+    const unsigned grid = (unsigned)std::min<int64_t>((items + rows - 1) / rows, kVfGrid);
+    hipError_t e;
+    if (greedy) {
+        if (items == 0)
+            ;
+        else if (wave)
+            hipLaunchKernelGGL((k_verify_best<T, 1>), dim3(grid), dim3(kBlock), 0, s, A);
+        else
+            hipLaunchKernelGGL((k_verify_best<T, 4>), dim3(grid), dim3(kBlock), 0, s, A);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL(k_verify_greedy, dim3((unsigned)std::min<int64_t>((A.b + 3) / 4, kVfGrid)), dim3(kBlock), 0, s, A);
+        return hipGetLastError();
+    }
+    if (items == 0)
+        ;
+    else if (wave)
+        hipLaunchKernelGGL((k_verify_sums<T, 1>), dim3(grid), dim3(kBlock), 0, s, A, kinds);
+    else
+        hipLaunchKernelGGL((k_verify_sums<T, 4>), dim3(grid), dim3(kBlock), 0, s, A, kinds);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((k_verify_chunks<T>), dim3((unsigned)std::min<int64_t>(A.b * A.parts, kVfGrid)), dim3(kBlock), 0, s, A);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((k_verify_draw<T>), dim3((unsigned)std::min<int64_t>(A.b, kVfGrid)), dim3(kBlock), 0, s, A);
+    return hipGetLastError();
+}
+
+bool good_sizes(int64_t n, int64_t m, int64_t b) {
+    return n >= 0 && n <= INT32_MAX && m >= 1 && m <= kVfMaxCols && b >= 0 && b <= INT32_MAX;
+}
+
+}  // namespace
+}  // namespace sk
+
+using namespace sk;
+
+extern "C" {
+
+size_t sk_scores_verify_workspace_bytes(int32_t dtype, int64_t n, int64_t m, int64_t b) {
+    if (dtype != SK_F32 && dtype != SK_BF16 && dtype != SK_F16) return 0;
+    return good_sizes(n, m, b) ? vf_plan(elem_size(dtype), n, m, b).total : 0;
+}
+
+int sk_scores_verify(const void* scores, int32_t dtype, int64_t n, int64_t m, int64_t ld, float eps, const void* draft,
+                     int64_t ld_draft, float eps_draft, const int64_t* tokens, const int64_t* starts, int64_t b,
+                     const float* u_accept, const float* u_sample, int32_t* accepted, int64_t* next, int64_t* out_tokens,
+                     float* ratio, float* logp, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_scores(scores, dtype, n, m, ld);
+    if (st) return st;
+    if (!good_sizes(n, m, b)) return SK_ERR_SHAPE;
+    if (draft && (st = check_scores(draft, dtype, n, m, ld_draft))) return st;
+    if (!std::isfinite(eps) || eps < 0.0f) return SK_ERR_EPS;
+    const bool greedy = eps == 0.0f;
+    if (draft && (!std::isfinite(eps_draft) || eps_draft <= 0.0f)) return SK_ERR_EPS;
+    const VfPlan P = vf_plan(elem_size(dtype), n, m, b);
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < P.total) return SK_ERR_WORKSPACE;
+    if (b == 0) return SK_OK;
+    if (!starts || !accepted || !next || (!greedy && !u_sample)) return SK_ERR_NULL;
+    if (n > 0 && (!tokens || !out_tokens || !ratio || !logp || (!greedy && !u_accept))) return SK_ERR_NULL;
+    char* base = static_cast<char*>(ws);
+    VfArgs A{};
+    A.s = scores;
+    A.q = greedy ? nullptr : draft;
+    A.ld = ld;
+    A.ldq = ld_draft;
+    A.n = n;
+    A.b = b;
+    A.m = (int)m;
+    A.c = greedy ? 1.0 : 1.4426950408889634074 / (double)eps;
+    A.cq = draft ? 1.4426950408889634074 / (double)eps_draft : 1.0;
+    A.tokens = tokens;
+    A.starts = starts;
+    A.u_accept = u_accept;
+    A.u_sample = u_sample;
+    A.accepted = accepted;
+    A.next = next;
+    A.out_tokens = out_tokens;
+    A.ratio = ratio;
+    A.logp = logp;
+    A.splits = P.splits;
+    A.cut = P.cut;
+    A.chunks = P.chunks;
+    A.parts = P.parts;
+    A.sums = reinterpret_cast<Sum*>(base + P.sums);
+    A.chunk = reinterpret_cast<double*>(base + P.chunk);
+    A.draw = reinterpret_cast<Draw*>(base + P.draw);
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    SK_TRY_LAUNCH(dtype == SK_F32 ? verify<F32>(A, greedy, s) : dtype == SK_BF16 ? verify<Bf16>(A, greedy, s) : verify<F16>(A, greedy, s));
+    return SK_OK;
+}
+
+}  // extern "C"
