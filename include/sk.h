@@ -611,7 +611,7 @@ int sk_scores_verify(const void *scores, int32_t dtype, int64_t n, int64_t m, in
  * What follows sk_scores_route: its choices sorted by expert, token rows brought into
  * that order, the experts' rows summed back, and the gradients.  A choice (i, r) of idx
  * (n, k) is numbered i k + r; k <= 64, m <= 1024 experts.  Token matrices are (n, d),
- * sorted ones (rows, d), of one sk_dtype, each with its own row stride >= d and
+ * d <= 2^28, sorted ones (rows, d), of one sk_dtype, each with its own row stride >= d and
  * aligned to its elements (any address and stride otherwise).  Products and sums are float32,
  * rounded once on output.  Outputs must not overlap inputs but where stated
  * (SK_ERR_OVERLAP).  Results are deterministic; all calls enqueue only (capturable).

@@ -25,7 +25,8 @@ constexpr int kRowsMaxTop = 64;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortMost = 16;      // pairs per thread at most: a wave's counter fits 16 bits
 constexpr int kSortOne = 4096;     // pairs that one workgroup takes alone
-constexpr int kSortGroups = 64;    // workgroups whose counts the others add up themselves
+// Workgroups whose counts the others add up themselves: 64, and up to 256 where that is no more than 16384 counts.
+int sort_groups(int64_t m) { return (int)std::min<int64_t>(256, std::max<int64_t>(64, 16384 / m)); }
 
 struct SortArgs {
     const int32_t* idx;
@@ -33,6 +34,7 @@ struct SortArgs {
     int m, bits, align, capacity;
     int per;  // pairs of a workgroup
     int groups, scanned;
+    int wide;  // power of two >= m
     int32_t *slot, *source, *counts, *offsets;
     int32_t* hist;  // [groups][m] counts of the workgroups (scanned: of those before), then [m] totals
 };
@@ -83,9 +85,28 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scan(SortArgs A) {
 template <int J>
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs A) {
     __shared__ uint16_t count[kSortWaves][kRowsMaxExperts];  // then: of the waves before
-    __shared__ int first[kRowsMaxExperts], stop[kRowsMaxExperts], before[kRowsMaxExperts];
+    __shared__ int first[kRowsMaxExperts], stop[kRowsMaxExperts], before[kRowsMaxExperts], all[kRowsMaxExperts];
     __shared__ int sums[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, group = blockIdx.x;
+    // the other workgroups' counts: each thread some of them for one expert, requested before all else
+    int prior = 0, total = 0;
+    if (A.groups > 1) {
+        const int q = tid & (A.wide - 1), parts = kSortThreads / A.wide;
+        if (A.scanned) {
+            if (tid < A.m) {
+                prior = A.hist[(int64_t)group * A.m + tid];
+                total = A.hist[(int64_t)A.groups * A.m + tid];
+            }
+        } else if (q < A.m) {
+#pragma unroll 16
+            for (int g = tid / A.wide; g < A.groups; g += parts) {
+                const int here = A.hist[g * A.m + q];
+                prior += g < group ? here : 0;
+                total += here;
+            }
+        }
+    }
+    for (int e = tid; e < A.m; e += kSortThreads) before[e] = all[e] = 0;
     for (int e = lane; e < A.m; e += 64) count[wave][e] = 0;
     wave_sync();
     const int64_t t0 = (int64_t)group * A.per + wave * (64 * J) + lane;
@@ -107,8 +128,13 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs A) {
         wave_sync();
     }
     __syncthreads();
-    // each thread an expert: its pairs in this workgroup, in those before, in all; then the segments' first rows
-    int total = 0, kept = 0, padded = 0;
+    if (A.groups > 1 && (tid & (A.wide - 1)) < A.m) {
+        atomicAdd(&before[tid & (A.wide - 1)], prior);
+        atomicAdd(&all[tid & (A.wide - 1)], total);
+    }
+    __syncthreads();
+    // each thread an expert: its pairs in this workgroup's waves, and in all; then the segments' first rows
+    int kept = 0, padded = 0;
     if (tid < A.m) {
         int run = 0;
 #pragma unroll
@@ -117,21 +143,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs A) {
             count[w][tid] = (uint16_t)run;
             run += here;
         }
-        int prior = 0;
-        if (A.groups == 1) {
-            total = run;
-        } else if (A.scanned) {
-            prior = A.hist[(int64_t)group * A.m + tid];
-            total = A.hist[(int64_t)A.groups * A.m + tid];
-        } else {
-#pragma unroll 8
-            for (int g = 0; g < A.groups; ++g) {
-                const int here = A.hist[g * A.m + tid];
-                prior += g < group ? here : 0;
-                total += here;
-            }
-        }
-        before[tid] = prior;
+        total = A.groups == 1 ? run : all[tid];
         kept = A.capacity ? min(total, A.capacity) : total;
         padded = (int)(((int64_t)kept + A.align - 1) / A.align * A.align);
     }
@@ -194,7 +206,7 @@ struct SortPlan {
 
 SortPlan sort_plan(int64_t pairs, int64_t m) {
     SortPlan P{1, 1, 0, 256};
-    const int64_t most = pairs <= kSortOne ? 1 : kSortGroups;
+    const int64_t most = pairs <= kSortOne ? 1 : sort_groups(m);
     while (P.per_thread < kSortMost && (int64_t)P.per_thread * kSortThreads * most < pairs) P.per_thread *= 2;
     const int64_t per = (int64_t)P.per_thread * kSortThreads;
     P.groups = (int)std::max<int64_t>(1, (pairs + per - 1) / per);
@@ -213,11 +225,14 @@ int64_t sort_rows(int64_t n, int32_t k, int64_t m, int32_t align, int32_t capaci
 }
 
 // ----- token rows -----------------------------------------------------------------------
+// A row goes in runs of 16 bytes at any address, and the elements behind its last whole run one by one.
+constexpr int64_t kRowsMaxCols = (int64_t)1 << 28;  // (32-bit offsets inside a row)
+
 struct RowsArgs {
-    int64_t n, d, rows;
-    int k, m;
-    int lanes;           // of a token: a power of two up to the workgroup
-    int64_t runs, span;  // runs of 16 bytes of a row, and those that one workgroup takes
+    int64_t n, rows;
+    int d, k, m;
+    int lanes;       // of a token: a power of two up to the workgroup
+    int runs, span;  // whole runs of 16 bytes of a row, and those that one workgroup takes
     int64_t token_groups;  // groups of kBlock / lanes tokens
     int64_t grid;          // workgroups that take them in turn
     const int32_t *slot, *counts, *offsets;
@@ -229,16 +244,33 @@ struct RowsArgs {
     float* d_weights;
 };
 
+__device__ __forceinline__ bool in_rows(const RowsArgs& A, int s) { return (uint64_t)(int64_t)s < (uint64_t)A.rows; }
+
+// f(first, last run, whether the elements behind the runs are taken too) for the workgroup's share of a row.
+struct Share {
+    int q0, q1;
+    bool rest;
+};
+__device__ __forceinline__ Share share_of(const RowsArgs& A) {
+    const int q0 = (int)blockIdx.y * A.span;
+    return {q0, min(A.runs, q0 + A.span), blockIdx.y + 1 == gridDim.y};
+}
+
 // The workgroups behind those of the tokens: one per expert, zeros into its segment's padding.
 template <class T>
 __device__ void clear_padding(const RowsArgs& A) {
+    using E = typename T::type;
     const int e = (int)(blockIdx.x - A.grid);
     const int64_t s0 = max((int64_t)A.offsets[e] + A.counts[e], (int64_t)0), s1 = min((int64_t)A.offsets[e + 1], A.rows);
+    const Share P = share_of(A);
     Run16<T> zero;
     zero.fill(0);
-    for (int64_t s = s0; s < s1; ++s)
-        for (int64_t q = blockIdx.y * A.span + threadIdx.x; q < min(A.runs, (blockIdx.y + 1) * A.span); q += kBlock)
-            zero.store(static_cast<typename T::type*>(A.out) + s * A.ld_out, q, A.d);
+    for (int64_t s = s0; s < s1; ++s) {
+        E* row = static_cast<E*>(A.out) + s * A.ld_out;
+        for (int q = P.q0 + threadIdx.x; q < P.q1; q += kBlock) zero.put(row + q * Run16<T>::n);
+        if (P.rest)
+            for (int j = A.runs * Run16<T>::n + threadIdx.x; j < A.d; j += kBlock) row[j] = E(0);
+    }
 }
 
 // f(token, lane in the token's group) for the thread's tokens.  ONE: all lanes of a wave have the same token.
@@ -254,34 +286,45 @@ __device__ __forceinline__ void each_token(const RowsArgs& A, F f) {
 }
 
 // rows[slot] = (w) x: a token's run is read once and stored to each of its rows.
-template <class T, bool ONE>
+// ONCE: the stores pass the caches by.
+template <class T, bool ONE, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_dispatch(RowsArgs A) {
     using E = typename T::type;
+    constexpr int VE = Run16<T>::n;
     if (blockIdx.x >= A.grid) return clear_padding<T>(A);
+    const Share P = share_of(A);
     each_token<ONE>(A, [&](int64_t i, int lane) {
         const E* x = static_cast<const E*>(A.tokens) + i * A.ld_tokens;
         const int32_t* slot = A.slot + i * A.k;
-        const int64_t q1 = min(A.runs, (blockIdx.y + 1) * A.span);
-        for (int64_t q = blockIdx.y * A.span + lane; q < q1; q += A.lanes) {
-            Run16<T> v;
-            v.load(x, q, A.d);
+        const float* weights = A.weights ? A.weights + i * A.k : nullptr;
+        auto each_row = [&](auto f) {
             for (int r = 0; r < A.k; ++r) {
                 const int s = slot[r];
-                if ((uint64_t)(int64_t)s >= (uint64_t)A.rows) continue;
-                E* row = static_cast<E*>(A.out) + s * A.ld_out;
-                if (A.weights) {
-                    const float w = A.weights[i * A.k + r];
-                    float o[Run16<T>::n];
-#pragma unroll
-                    for (int c = 0; c < Run16<T>::n; ++c) o[c] = w * v.at(c);
-                    Run16<T> scaled;
-                    scaled.round(o);
-                    scaled.store(row, q, A.d);
-                } else {
-                    v.store(row, q, A.d);
-                }
+                if (in_rows(A, s)) f(static_cast<E*>(A.out) + s * A.ld_out, weights ? weights[r] : 1.0f);
             }
+        };
+        for (int q = P.q0 + lane; q < P.q1; q += A.lanes) {
+            Run16<T> v;
+            v.get(x + q * VE);
+            each_row([&](E* row, float w) {
+                Run16<T> o = v;
+                if (weights) {
+                    float f[VE];
+#pragma unroll
+                    for (int c = 0; c < VE; ++c) f[c] = w * v.at(c);
+                    o.round(f);
+                }
+                if constexpr (ONCE)
+                    o.put_once(row + q * VE);
+                else
+                    o.put(row + q * VE);
+            });
         }
+        if (P.rest)
+            for (int j = A.runs * VE + lane; j < A.d; j += A.lanes) {
+                const E v = x[j];
+                each_row([&](E* row, float w) { row[j] = weights ? T::from(w * T::to(v)) : v; });
+            }
     });
 }
 
@@ -292,33 +335,48 @@ template <class T, bool ONE>
 __global__ __launch_bounds__(kBlock) void k_combine(RowsArgs A) {
     using E = typename T::type;
     constexpr int VE = Run16<T>::n;
+    const Share P = share_of(A);
     each_token<ONE>(A, [&](int64_t i, int lane) {
         const int32_t* slot = A.slot + i * A.k;
-        const int64_t q1 = min(A.runs, (blockIdx.y + 1) * A.span);
-        for (int64_t q = blockIdx.y * A.span + lane; q < q1; q += A.lanes) {
+        const float* weights = A.weights ? A.weights + i * A.k : nullptr;
+        const E* add = A.add ? static_cast<const E*>(A.add) + i * A.ld_add : nullptr;
+        E* out = static_cast<E*>(A.out) + i * A.ld_out;
+        for (int q = P.q0 + lane; q < P.q1; q += A.lanes) {
             float y[VE];
             Run16<T> v[kAhead];
-            if (A.add) v[0].load(static_cast<const E*>(A.add) + i * A.ld_add, q, A.d);
+            if (add) v[0].get(add + q * VE);
 #pragma unroll
-            for (int c = 0; c < VE; ++c) y[c] = A.add ? v[0].at(c) : 0.0f;
+            for (int c = 0; c < VE; ++c) y[c] = add ? v[0].at(c) : 0.0f;
             for (int r0 = 0; r0 < A.k; r0 += kAhead) {
                 float w[kAhead];
 #pragma unroll
                 for (int r = 0; r < kAhead; ++r) {
                     const int s = r0 + r < A.k ? slot[r0 + r] : -1;
-                    const bool in = (uint64_t)(int64_t)s < (uint64_t)A.rows;
-                    w[r] = !in ? 0.0f : A.weights ? A.weights[i * A.k + r0 + r] : 1.0f;
+                    const bool in = in_rows(A, s);
+                    w[r] = !in ? 0.0f : weights ? weights[r0 + r] : 1.0f;
                     v[r].fill(0);
-                    if (in) v[r].load(static_cast<const E*>(A.in) + s * A.ld_in, q, A.d);
+                    if (in) v[r].get_once(static_cast<const E*>(A.in) + s * A.ld_in + q * VE);
                 }
 #pragma unroll
-                for (int r = 0; r < kAhead; ++r)
+                for (int r = 0; r < kAhead; ++r) {
+                    v[r].held();
 #pragma unroll
                     for (int c = 0; c < VE; ++c) y[c] = fmaf(w[r], v[r].at(c), y[c]);
+                }
             }
             v[0].round(y);
-            v[0].store(static_cast<E*>(A.out) + i * A.ld_out, q, A.d);
+            v[0].put_once(out + q * VE);
         }
+        if (P.rest)
+            for (int j = A.runs * VE + lane; j < A.d; j += A.lanes) {
+                float y = add ? T::to(add[j]) : 0.0f;
+                for (int r = 0; r < A.k; ++r) {
+                    const int s = slot[r];
+                    if (in_rows(A, s))
+                        y = fmaf(weights ? weights[r] : 1.0f, T::to(static_cast<const E*>(A.in)[s * A.ld_in + j]), y);
+                }
+                out[j] = T::from(y);
+            }
     });
 }
 
@@ -340,22 +398,22 @@ __global__ __launch_bounds__(kBlock) void k_combine_grad(RowsArgs A) {
         const int32_t* slot = A.slot + i * A.k;
         for (int r0 = 0; r0 < A.k; r0 += kAhead) {
             float dot[kAhead], w[kAhead];
-            int64_t s[kAhead];
+            int s[kAhead];
 #pragma unroll
             for (int r = 0; r < kAhead; ++r) {
-                const int row = r0 + r < A.k ? slot[r0 + r] : -1;
-                s[r] = (uint64_t)(int64_t)row < (uint64_t)A.rows ? row : -1;
+                s[r] = r0 + r < A.k ? slot[r0 + r] : -1;
+                if (!in_rows(A, s[r])) s[r] = -1;
                 w[r] = s[r] < 0 ? 0.0f : A.weights ? A.weights[i * A.k + r0 + r] : 1.0f;
                 dot[r] = 0.0f;
             }
-            for (int64_t q = lane; q < A.runs; q += L) {
+            for (int q = lane; q < A.runs; q += L) {
                 Run16<T> dyr, v[kAhead];
-                dyr.load(dy, q, A.d);
+                dyr.get(dy + q * VE);
                 if (A.d_weights) {
 #pragma unroll
                     for (int r = 0; r < kAhead; ++r) {
                         v[r].fill(0);
-                        if (s[r] >= 0) v[r].load(static_cast<const E*>(A.in) + s[r] * A.ld_in, q, A.d);
+                        if (s[r] >= 0) v[r].get_once(static_cast<const E*>(A.in) + s[r] * A.ld_in + q * VE);
                     }
                 }
                 float gf[VE];
@@ -365,6 +423,7 @@ __global__ __launch_bounds__(kBlock) void k_combine_grad(RowsArgs A) {
                 for (int r = 0; r < kAhead; ++r) {
                     if (s[r] < 0) continue;
                     if (A.d_weights) {
+                        v[r].held();
 #pragma unroll
                         for (int c = 0; c < VE; ++c) dot[r] = fmaf(v[r].at(c), gf[c], dot[r]);
                     }
@@ -374,8 +433,17 @@ __global__ __launch_bounds__(kBlock) void k_combine_grad(RowsArgs A) {
                         for (int c = 0; c < VE; ++c) o[c] = w[r] * gf[c];
                         Run16<T> scaled;
                         scaled.round(o);
-                        scaled.store(static_cast<E*>(A.out) + s[r] * A.ld_out, q, A.d);
+                        scaled.put(static_cast<E*>(A.out) + s[r] * A.ld_out + q * VE);
                     }
+                }
+            }
+            for (int j = A.runs * VE + lane; j < A.d; j += L) {
+                const float gf = T::to(dy[j]);
+#pragma unroll
+                for (int r = 0; r < kAhead; ++r) {
+                    if (s[r] < 0) continue;
+                    if (A.d_weights) dot[r] = fmaf(T::to(static_cast<const E*>(A.in)[s[r] * A.ld_in + j]), gf, dot[r]);
+                    if (A.out && on) static_cast<E*>(A.out)[s[r] * A.ld_out + j] = T::from(w[r] * gf);
                 }
             }
             if (!A.d_weights) continue;
@@ -403,7 +471,7 @@ __global__ __launch_bounds__(kBlock) void k_combine_grad(RowsArgs A) {
 }
 
 // ----- host side ------------------------------------------------------------------------
-int lanes_for(int64_t runs, int least) {
+int lanes_for(int runs, int least) {
     int lanes = least;
     while (lanes < kBlock && lanes < runs) lanes *= 2;
     return lanes;
@@ -416,34 +484,36 @@ void share(RowsArgs& A, int lanes) {
     const int per = kBlock / lanes;
     A.token_groups = (A.n + per - 1) / per;
     A.grid = std::min(A.token_groups, kRowsGrid);
-    A.span = A.runs;
+    A.span = std::max(A.runs, 1);
 }
 
 template <class K>
 hipError_t launch_rows(const RowsArgs& A, K kernel, bool pads, hipStream_t s) {
     const int64_t groups = A.grid + (pads ? A.m : 0);
-    const int64_t parts = (A.runs + A.span - 1) / A.span;
+    const int parts = std::max(1, (A.runs + A.span - 1) / A.span);
     hipLaunchKernelGGL(kernel, dim3((unsigned)groups, (unsigned)parts), dim3(kBlock), 0, s, A);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t dispatch(RowsArgs A, hipStream_t s) {
-    A.runs = (A.d + Run16<T>::n - 1) / Run16<T>::n;
+    A.runs = A.d / Run16<T>::n;
     share(A, lanes_for(A.runs, 8));
-    return launch_rows(A, A.lanes >= 64 ? k_dispatch<T, true> : k_dispatch<T, false>, A.counts != nullptr, s);
+    const bool aligned = reinterpret_cast<uintptr_t>(A.out) % 16 == 0 && A.ld_out % Run16<T>::n == 0;
+    auto kernel = A.lanes < 64 ? k_dispatch<T, false, false> : aligned ? k_dispatch<T, true, true> : k_dispatch<T, true, false>;
+    return launch_rows(A, kernel, A.counts != nullptr, s);
 }
 
 template <class T>
 hipError_t combine(RowsArgs A, hipStream_t s) {
-    A.runs = (A.d + Run16<T>::n - 1) / Run16<T>::n;
+    A.runs = A.d / Run16<T>::n;
     share(A, lanes_for(A.runs, 8));
     return launch_rows(A, A.lanes >= 64 ? k_combine<T, true> : k_combine<T, false>, false, s);
 }
 
 template <class T>
 hipError_t combine_grad(RowsArgs A, hipStream_t s) {
-    A.runs = (A.d + Run16<T>::n - 1) / Run16<T>::n;
+    A.runs = A.d / Run16<T>::n;
     share(A, A.runs <= 16 ? 16 : A.runs <= 128 ? 64 : 256);
     auto kernel = A.lanes == 16 ? k_combine_grad<T, 16> : A.lanes == 64 ? k_combine_grad<T, 64> : k_combine_grad<T, 256>;
     return launch_rows(A, kernel, A.out && A.counts, s);
@@ -462,7 +532,7 @@ bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 // Sizes shared by the three row operators.
 int check_rows(int32_t dtype, int64_t n, int64_t d, int32_t k, int64_t rows) {
     if (dtype != SK_F32 && dtype != SK_BF16 && dtype != SK_F16) return SK_ERR_DTYPE;
-    if (n < 0 || n > INT32_MAX || d < 1 || d > INT32_MAX || rows < 0 || rows > INT32_MAX) return SK_ERR_SHAPE;
+    if (n < 0 || n > INT32_MAX || d < 1 || d > kRowsMaxCols || rows < 0 || rows > INT32_MAX) return SK_ERR_SHAPE;
     if (k < 1 || k > kRowsMaxTop) return SK_ERR_ROUTE;
     return SK_OK;
 }
@@ -516,7 +586,9 @@ int sk_route_sort(const int32_t* idx, int64_t n, int32_t k, int64_t m, int32_t a
     A.capacity = capacity;
     A.per = P.per_thread * kSortThreads;
     A.groups = P.groups;
-    A.scanned = P.groups > kSortGroups;
+    A.scanned = P.groups > sort_groups(m);
+    A.wide = 1;
+    while (A.wide < m) A.wide *= 2;
     A.slot = slot;
     A.source = source;
     A.counts = counts;
@@ -550,7 +622,7 @@ int sk_route_dispatch(const void* x, int32_t dtype, int64_t n, int64_t d, int64_
     if (meet(span_of(x, n, d, ld, elem_size(dtype)), span_of(out, rows, d, ld_out, elem_size(dtype)))) return SK_ERR_OVERLAP;
     RowsArgs A{};
     A.n = n;
-    A.d = d;
+    A.d = (int)d;
     A.rows = rows;
     A.k = k;
     A.m = (int)m;
@@ -583,7 +655,7 @@ int sk_route_combine(const void* in, int32_t dtype, int64_t rows, int64_t d, int
     if (add && !in_place && meet(span_of(add, n, d, ld_add, es), out)) return SK_ERR_OVERLAP;
     RowsArgs A{};
     A.n = n;
-    A.d = d;
+    A.d = (int)d;
     A.rows = rows;
     A.k = k;
     A.slot = slot;
@@ -620,7 +692,7 @@ int sk_route_combine_grad(const void* in, int32_t dtype, int64_t rows, int64_t d
     }
     RowsArgs A{};
     A.n = n;
-    A.d = d;
+    A.d = (int)d;
     A.rows = rows;
     A.k = k;
     A.m = (int)m;

@@ -231,6 +231,18 @@ struct Run16 {
     }
     __device__ __forceinline__ void fill(uint32_t w) { raw = make_uint4(w, w, w, w); }
     __device__ __forceinline__ void get(const Elem* p) { __builtin_memcpy(&raw, p, 16); }
+    // The same for what this launch touches once: not to push out what the caches hold.
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    typedef Words AnyWords __attribute__((aligned(2)));
+    __device__ __forceinline__ void get_once(const Elem* p) {
+        const Words w = __builtin_nontemporal_load(reinterpret_cast<const AnyWords*>(p));
+        raw = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void put_once(Elem* p) const {
+        __builtin_nontemporal_store(Words{raw.x, raw.y, raw.z, raw.w}, reinterpret_cast<AnyWords*>(p));
+    }
+    // Holds the run as it was loaded up to here: its conversions to float32, twice the registers, stay behind.
+    __device__ __forceinline__ void held() { asm("" : "+v"(raw.x), "+v"(raw.y), "+v"(raw.z), "+v"(raw.w)); }
     __device__ __forceinline__ void put(Elem* p) const { __builtin_memcpy(p, &raw, 16); }
     // Run q of a row of d elements: behind the row's end the elements read as 0 and are not written.
     __device__ __forceinline__ void load(const Elem* row, int64_t q, int64_t d) {

@@ -8,9 +8,9 @@
 // p, the transport plan of least cost 1[x != y].
 //
 // A decision or a draw next to a border must not depend on how sums are taken, so
-// exponentials and sums are in float64 throughout (a float64 FMA issues as fast as
-// a float32 one here): the error of a probability is some 2^-49 of it, where a row of
-// 131072 has borders 2^-20 apart and the random numbers are multiples of 2^-24.
+// exponentials and sums are in float64 throughout: the error of a probability is
+// some 2^-38 of it, where a row of 131072 has borders 2^-17 apart in the mean and the
+// random numbers are multiples of 2^-24.
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -20,8 +20,8 @@ namespace {
 
 constexpr int64_t kVfGrid = 1 << 20;  // workgroups of one launch (each may serve several rows)
 constexpr int64_t kVfMaxCols = (int64_t)1 << 30;
-constexpr int kVfVecs = 4;            // 16-byte loads of a thread's block
-constexpr int kVfChunk = 2048;        // entries of the residual whose sum is kept
+constexpr int kVfVecs = 4;             // 16-byte loads of a thread's block
+constexpr int kVfChunkMost = 2048;    // entries of the residual whose sum is kept: 512, 1024 or 2048
 constexpr int kVfFill = 1024, kVfCutMin = 1024;
 constexpr double kFloor = -1000.0;    // exponents below count as zero
 constexpr double kUnset = -1.0e300;   // reference of a part without an unmasked entry
@@ -52,37 +52,46 @@ struct VfArgs {
     int64_t *next, *out_tokens;
     float *ratio, *logp;
     int splits, cut;  // parts of a row, and the runs of 16 bytes of one
-    int chunks, parts;
+    int width;        // lanes that join a row's parts: a power of two
+    int chunk_len, chunks, parts;
     Sum* sums;        // [n][2][splits]
     double* chunk;    // [b][chunks]
     Draw* draw;       // [b]
 };
 
 // 2^(d c) for d c in [kFloor, 1000]: the exponent is k + f with |f| <= 1/2, 2^f by the polynomial that meets it at the
-// ten Chebyshev points and at 0 (within 2^-50.6), k added to the exponent.  2^0 is 1 exactly.
+// eight Chebyshev points and at 0 (within 2^-38.7), k added to the exponent.  2^0 is 1 exactly.
 __device__ __forceinline__ double pow2(double d, double c) {
     constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52: the sum's low word is the nearest integer
     const double t = fma(d, c, kRound);
     const double f = fma(d, c, -(t - kRound));
-    double p = 0x1.e5e9f548e5725p-28;
-    p = fma(p, f, 0x1.b6571de2f2351p-24);
-    p = fma(p, f, 0x1.62bfe46117445p-20);
-    p = fma(p, f, 0x1.ffcb76789860fp-17);
-    p = fma(p, f, 0x1.4309130378460p-13);
-    p = fma(p, f, 0x1.5d87fe908f88ap-10);
-    p = fma(p, f, 0x1.3b2ab6fba385fp-7);
-    p = fma(p, f, 0x1.c6b08d7044119p-5);
-    p = fma(p, f, 0x1.ebfbdff82c590p-3);
-    p = fma(p, f, 0x1.62e42fefa39f7p-1);
+    double p = 0x1.63b2d7971923fp-20;
+    p = fma(p, f, 0x1.00c0e4e15189cp-16);
+    p = fma(p, f, 0x1.4308c7183d6a2p-13);
+    p = fma(p, f, 0x1.5d877598350dep-10);
+    p = fma(p, f, 0x1.3b2ab70ad2565p-7);
+    p = fma(p, f, 0x1.c6b08da70cce3p-5);
+    p = fma(p, f, 0x1.ebfbdff82a734p-3);
+    p = fma(p, f, 0x1.62e42fef9cc69p-1);
     p = fma(p, f, 1.0);
     const uint64_t bits = __builtin_bit_cast(uint64_t, p);
     const uint32_t k = (uint32_t)__builtin_bit_cast(uint64_t, t);
-    return __builtin_bit_cast(double, bits + ((uint64_t)k << 52));
+    const uint32_t high = (uint32_t)(bits >> 32) + (k << 20);
+    return __builtin_bit_cast(double, (uint64_t)high << 32 | (uint32_t)bits);
 }
 // 2^y; 0 below the floor (a masked score's exponent is -inf).
 __device__ __forceinline__ double pow2_or_zero(double y) {
     const double v = pow2(fmax(y, kFloor), 1.0);
     return y > kFloor ? v : 0.0;
+}
+
+// log2 of x > 0: float32's logarithm of the mantissa, and one step from what 2 to that power leaves of it.
+__device__ __forceinline__ double log2_of(double x) {
+    const int e = __builtin_amdgcn_frexp_exp(x);
+    const double m = __builtin_amdgcn_frexp_mant(x);  // [1/2, 1)
+    const double guess = (double)s_lg2((float)m);
+    const double z = fma(m, pow2(-guess, 1.0), -1.0);  // some 2^-22
+    return (double)e + (guess + z * fma(z, -0.7213475204444817, 1.4426950408889634));
 }
 
 // A sum taken to another, no lower reference; an unset one is 0 there.
@@ -100,10 +109,11 @@ __device__ __forceinline__ Sum lanes_join(Sum a, double c) {
     return {ref, lanes_sum<L>(moved(a, ref, c))};
 }
 
-// Whether row i of the target is one that a request looks at.  All lanes of a wave, i the same in each.
-__device__ bool row_counts(const VfArgs& A, int64_t i, int lane) {
-    if (i < A.starts[0] || i >= A.starts[A.b]) return false;
-    if (i > 0 && A.tokens[i - 1] >= 0) return true;
+// Whether row i of the target (of the draft) is one that a request looks at.  All lanes of a wave, i the same in each.
+__device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draft, int lane) {
+    const int64_t lowest = A.starts[0], end = A.starts[A.b], here = A.tokens[i], before = A.tokens[i > 0 ? i - 1 : 0];
+    if (i < lowest || i >= end || (draft && here < 0)) return false;
+    if (i > 0 && before >= 0) return true;
     // behind a row without a drafted token only a request's first row counts: a search by 64 at a time
     int64_t lo = 0, size = A.b;
     while (size > 64) {
@@ -120,20 +130,16 @@ __device__ bool row_counts(const VfArgs& A, int64_t i, int lane) {
 
 // Sums of the rows' exponentials: a row, or a part of one, per W waves.
 template <class T, int W>
-__global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A, int kinds) {
+__global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
     using E = typename T::type;
     constexpr int VE = Run16<T>::n, kThreads = W * 64, kRows = kBlock / kThreads, NV = kVfVecs, kStep = kThreads * NV;
     __shared__ Sum red[kBlock / 64];
     const int t = threadIdx.x % kThreads, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
-    const int64_t items = A.n * A.splits * kinds;
-    for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items; item0 += (int64_t)gridDim.x * kRows) {
-        const int64_t item = item0 + slot;
-        if (item >= items) return;  // (one wave per row: no barrier below)
-        const int64_t i = item / (A.splits * kinds);
-        const int kind = (int)(item / A.splits % kinds), split = (int)(item % A.splits);
-        const bool draft = kind == 1;
-        if ((draft && A.tokens[i] < 0) || !row_counts(A, i, lane)) continue;
+    // the grid's second dimension: parts of a row, of the target's and then of the draft's
+    const int kind = blockIdx.y >= (unsigned)A.splits, split = (int)blockIdx.y - kind * A.splits;
+    const bool draft = kind == 1;
+    for (int64_t i = (int64_t)blockIdx.x * kRows + slot; i < A.n; i += (int64_t)gridDim.x * kRows) {
         const E* row = static_cast<const E*>(draft ? A.q : A.s) + i * (draft ? A.ldq : A.ld);
         const double c = draft ? A.cq : A.c;
         const int runs = A.m / VE, tail = A.m - runs * VE;
@@ -144,7 +150,8 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A, int kinds) {
 #pragma unroll
             for (int q = 0; q < NV; ++q) next[q].get(row + (int64_t)min(v0 + b * kStep + q * kThreads + t, v1 - 1) * VE);
         };
-        if (blocks > 0) fetch(0);
+        if (blocks > 0) fetch(0);  // (before it is known whether the row counts)
+        if (!row_counts(A, i, draft, lane)) continue;
         double ref = 0.0, S = 0.0;
         const double floor = kFloor / c;
         float limit = -INFINITY;  // a larger score moves the reference
@@ -208,29 +215,9 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A, int kinds) {
 struct RowLog {
     double ref, log_sum;  // -inf: no unmasked entry; NaN: a NaN or +inf score
 };
-__device__ __forceinline__ RowLog row_log(const VfArgs& A, int64_t i, int kind) {
-    const Sum* p = A.sums + (i * 2 + kind) * A.splits;
-    Sum sum = p[0];
-    for (int k = 1; k < A.splits; ++k) sum = join(sum, p[k], kind ? A.cq : A.c);
-    return {sum.ref, sum.s == 0.0 ? -(double)INFINITY : log2(sum.s)};
-}
-template <class T>
-__device__ __forceinline__ double column_log(const void* m, int64_t ld, int64_t i, int64_t j, double c, const RowLog& r) {
-    const float s = T::to(static_cast<const typename T::type*>(m)[i * ld + j]);
+__device__ __forceinline__ double column_log(float s, double c, const RowLog& r) {
     if (r.log_sum != r.log_sum) return r.log_sum;
     return s == -INFINITY ? -(double)INFINITY : fma((double)s - r.ref, c, -r.log_sum);
-}
-
-// p(x) / q(x) of row i's drafted token x, at most 1; NaN where one of the rows holds a NaN or +inf.
-template <class T>
-__device__ __forceinline__ double ratio_of(const VfArgs& A, int64_t i, int64_t token, const RowLog& p, const RowLog& q) {
-    const bool in = token < A.m;  // a token that the vocabulary does not have: p is 0
-    const double lp = in ? column_log<T>(A.s, A.ld, i, token, A.c, p) : -(double)INFINITY;
-    const double lq = !A.q ? 0.0 : in ? column_log<T>(A.q, A.ldq, i, token, A.cq, q) : q.log_sum;
-    if (p.log_sum != p.log_sum || lq != lq) return (double)NAN;
-    if (lp < kFloor) return 0.0;
-    const double d = lp - lq;
-    return d >= 0.0 || lq < kFloor ? 1.0 : exp2(d);
 }
 
 struct Rows {
@@ -241,50 +228,98 @@ __device__ __forceinline__ Rows rows_of(const VfArgs& A, int64_t r) {
     return {lo, hi};
 }
 
-// Where a request stops, by all lanes of a wave: the first row whose token is not taken or that has none.
+struct Look {
+    RowLog row[2][64];
+    Draw draw;
+    int stop, none;  // in a block of 64 rows: the first that is not taken, that has no drafted token; 64: not there
+};
+
+// Where a request stops, by a whole workgroup: the first row whose token is not taken or that has none.  64 rows at a
+// time: A.width lanes join the parts of a row's sum, then a wave has a row per lane.  With write, the request's outputs
+// but what is drawn; the row where it stops keeps its drafted token until then, for the other workgroups that look at it.
 template <class T>
-__device__ Draw stop_of(const VfArgs& A, int64_t r, int lane) {
-    Draw d{0.0, 0.0, 0.0, 0.0, -1, -1, 0};
+__device__ Draw look(const VfArgs& A, int64_t r, bool write, Look& L) {
+    using E = typename T::type;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, kinds = A.q ? 2 : 1;
     const Rows R = rows_of(A, r);
+    Draw d{0.0, 0.0, 0.0, 0.0, -1, -1, 0};
+    bool stopped = false, ended = false;
     for (int64_t i0 = R.lo; i0 < R.hi; i0 += 64) {
+        const int rows = (int)min((int64_t)64, R.hi - i0);
         const int64_t i = i0 + lane;
-        int64_t token = -1;
-        RowLog p{0.0, 0.0}, q{0.0, 0.0};
-        bool stop = false;
-        if (i < R.hi) {
-            // rows behind one without a drafted token have no sums; they lie behind the stop
+        const bool on = wave == 0 && lane < rows;
+        int64_t token = 0;
+        float s = 0.0f, q = 0.0f, u = 0.0f;
+        bool known = false;  // a token of the vocabulary
+        if (on) {
             token = A.tokens[i];
-            p = row_log(A, i, 0);
-            if (A.q && token >= 0) q = row_log(A, i, 1);
-            if (token >= 0) {
-                const double ratio = ratio_of<T>(A, i, token, p, q);
-                stop = !((double)A.u_accept[i] < ratio && ratio > 0.0);
-            } else {
-                stop = true;
+            u = A.u_accept[i];
+            known = token >= 0 && token < A.m;
+            if (known) s = T::to(static_cast<const E*>(A.s)[i * A.ld + token]);
+            if (known && A.q) q = T::to(static_cast<const E*>(A.q)[i * A.ldq + token]);
+        }
+        // (rows behind one without a drafted token, and draft rows of one, have no sums and are not looked at)
+        for (int item = tid / A.width; item < rows * kinds; item += kBlock / A.width) {
+            const int row = item / kinds, kind = item % kinds, part = tid % A.width;
+            const double c = kind ? A.cq : A.c;
+            const Sum* p = A.sums + ((i0 + row) * 2 + kind) * A.splits;
+            Sum sum = part < A.splits ? p[part] : Sum{kUnset, 0.0};
+            for (int k = part + A.width; k < A.splits; k += A.width) sum = join(sum, p[k], c);
+            double ref = sum.ref;
+            for (int o = 1; o < A.width; o *= 2) ref = fmax(ref, __shfl_xor(ref, o));
+            double all = moved(sum, ref, c);
+            for (int o = 1; o < A.width; o *= 2) all += __shfl_xor(all, o);
+            if (part == 0) L.row[kind][row] = {ref, all == 0.0 ? -(double)INFINITY : all != all ? all : log2_of(all)};
+        }
+        __syncthreads();
+        if (wave == 0) {
+            const RowLog P = L.row[0][lane], Q = L.row[A.q ? 1 : 0][lane];
+            const double lp = known ? column_log(s, A.c, P) : P.log_sum == P.log_sum ? -(double)INFINITY : P.log_sum;
+            const double lq = !A.q ? 0.0 : known ? column_log(q, A.cq, Q) : Q.log_sum;
+            // p(x) / q(x), at most 1; NaN where one of the rows holds a NaN or +inf
+            const double gap = lp - lq;
+            const double ratio = lp != lp || lq != lq ? (double)NAN
+                                 : lp < kFloor        ? 0.0
+                                 : gap >= 0.0 || lq < kFloor ? 1.0
+                                                             : pow2_or_zero(gap);
+            const bool taken = token >= 0 && (double)u < ratio && ratio > 0.0;
+            const uint64_t stops = __ballot(on && !taken), nones = __ballot(on && token < 0);
+            const int stop = stops ? __ffsll((unsigned long long)stops) - 1 : 64;
+            const int none = nones ? __ffsll((unsigned long long)nones) - 1 : 64;
+            if (lane == stop)
+                L.draw = {P.ref, P.log_sum, Q.ref, Q.log_sum, i, A.q || !known ? -1 : token, A.q && token >= 0};
+            if (lane == 0) L.stop = stop, L.none = none;
+            if (write && on) {
+                const bool emits = !stopped && lane < stop;
+                if (stopped || lane > stop) A.out_tokens[i] = -1;
+                if (emits) A.out_tokens[i] = token;
+                A.ratio[i] = ended || lane >= none ? 0.0f : (float)ratio;
+                A.logp[i] = emits ? (float)(lp * 0.6931471805599453094) : 0.0f;
             }
         }
-        const uint64_t mask = __ballot(stop);
-        if (!mask) continue;
-        const int at = __ffsll((unsigned long long)mask) - 1;
-        d.row = i0 + at;
-        d.ref_p = __shfl(p.ref, at);
-        d.ref_q = __shfl(q.ref, at);
-        d.log_p = __shfl(p.log_sum, at);
-        d.log_q = __shfl(q.log_sum, at);
-        token = __shfl((long long)token, at);
-        d.with_q = A.q && token >= 0;
-        d.out = !A.q && token >= 0 && token < A.m ? token : -1;
-        break;
+        __syncthreads();
+        if (!stopped && L.stop < 64) {
+            d = L.draw;
+            stopped = true;
+        }
+        ended = ended || L.none < 64;
+        __syncthreads();
+        if (stopped && !write) break;
+    }
+    if (write && tid == 0) {
+        A.accepted[r] = (int32_t)((stopped ? d.row : R.hi) - R.lo);
+        A.next[r] = -1;
     }
     return d;
 }
 
 // An entry of what is drawn from: max(p - q, 0), or, where no draft scores take part, p relative to its reference.
+// (An exponent that is NaN, that of a draft row without an unmasked entry, counts as zero too.)
 template <class T>
 __device__ __forceinline__ double weight(const VfArgs& A, const Draw& d, float s, float t, int64_t j) {
     if (d.with_q) {
         const double p = pow2_or_zero(fma((double)s - d.ref_p, A.c, -d.log_p));
-        const double q = t == -INFINITY ? 0.0 : pow2_or_zero(fma((double)t - d.ref_q, A.cq, -d.log_q));
+        const double q = pow2_or_zero(fma((double)t - d.ref_q, A.cq, -d.log_q));
         return fmax(p - q, 0.0);
     }
     return j == d.out ? 0.0 : pow2_or_zero(((double)s - d.ref_p) * A.c);
@@ -298,43 +333,33 @@ __device__ __forceinline__ bool drawable(const Draw& d) {
 template <class T>
 __device__ __forceinline__ double chunk_sum(const VfArgs& A, const Draw& d, int chunk, int lane) {
     using E = typename T::type;
-    constexpr int VE = Run16<T>::n, NV = kVfChunk / 64 / VE;
-    const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
-    const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
-    const int j0 = chunk * kVfChunk;
+    constexpr int VE = Run16<T>::n;
+    const int start = chunk * A.chunk_len, j0 = start + lane * VE, size = min(A.chunk_len, A.m - start);
+    const E* s = static_cast<const E*>(A.s) + d.row * A.ld + j0;
+    const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld) + j0;
     double sum = 0.0;
-    if (A.m - j0 >= kVfChunk) {
-        Run16<T> a[NV], b[NV];
+    if (size == A.chunk_len) {
+        Run16<T> a, b, a1, b1;
+        a1.get(s);
+        b1.get(q);
+#pragma unroll 1
+        for (int at = 0; at < size; at += 64 * VE) {
+            a = a1;
+            b = b1;
+            const int next = at + 64 * VE < size ? at + 64 * VE : at;
+            a1.get(s + next);
+            b1.get(q + next);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            a[v].get(s + j0 + (v * 64 + lane) * VE);
-            b[v].get(q + j0 + (v * 64 + lane) * VE);
+            for (int e = 0; e < VE; ++e) sum += weight<T>(A, d, a.at(e), b.at(e), j0 + at + e);
         }
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) sum += weight<T>(A, d, a[v].at(e), b[v].at(e), j0 + (v * 64 + lane) * VE + e);
     } else {
-        for (int64_t j = j0 + lane; j < A.m; j += 64) sum += weight<T>(A, d, T::to(s[j]), T::to(q[j]), j);
+#pragma unroll 1
+        for (int at = 0; at < size; at += 64 * VE)
+#pragma unroll 1
+            for (int e = 0; e < VE && at + lane * VE + e < size; ++e)
+                sum += weight<T>(A, d, T::to(s[at + e]), T::to(q[at + e]), j0 + at + e);
     }
     return lanes_sum<64>(sum);
-}
-
-// Sums of the chunks of what each request draws from: a wave per chunk, A.parts workgroups per request.
-template <class T>
-__global__ __launch_bounds__(kBlock) void k_verify_chunks(VfArgs A) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    for (int64_t item = blockIdx.x; item < A.b * A.parts; item += gridDim.x) {
-        const int64_t r = item / A.parts;
-        const int part = (int)(item % A.parts);
-        const Draw d = stop_of<T>(A, r, lane);
-        if (part == 0 && threadIdx.x == 0) A.draw[r] = d;
-        if (!drawable(d)) continue;
-        for (int k = part * (kBlock / 64) + wave; k < A.chunks; k += A.parts * (kBlock / 64)) {
-            const double sum = chunk_sum<T>(A, d, k, lane);
-            if (lane == 0) A.chunk[r * A.chunks + k] = sum;
-        }
-    }
 }
 
 // Inclusive sums over the workgroup's threads; the last is the same in every thread.
@@ -357,134 +382,156 @@ __device__ __forceinline__ double block_scan(double x, double* lds, double& tota
     return before + x;
 }
 
-// The draw and a request's outputs: one workgroup per request.
+struct Pick {
+    double scan[kBlock / 64], prior;
+    uint64_t over[kBlock / 64], some[kBlock / 64];
+};
+
+// Of the threads for which over holds the first, else the last of those for which some does (-1: none), in every thread.
+__device__ __forceinline__ int first_over(bool over, bool some, Pick& L, bool& found) {
+    const uint64_t a = __ballot(over), b = __ballot(some);
+    const int wave = threadIdx.x / 64;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) L.over[wave] = a, L.some[wave] = b;
+    __syncthreads();
+    int first = -1, last = -1;
+#pragma unroll
+    for (int w = 0; w < kBlock / 64; ++w) {
+        const uint64_t x = L.over[w], y = L.some[w];
+        if (first < 0 && x) first = w * 64 + __ffsll((unsigned long long)x) - 1;
+        if (y) last = w * 64 + 63 - __clzll((long long)y);
+    }
+    found = first >= 0;
+    return found ? first : last;
+}
+
+// The draw of a request from its chunks' sums, by a whole workgroup.
 template <class T>
-__global__ __launch_bounds__(kBlock) void k_verify_draw(VfArgs A) {
+__device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
     using E = typename T::type;
-    __shared__ double lds[kBlock / 64];
-    __shared__ int found, last;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    constexpr int kPer = kVfChunk / kBlock;
-    for (int64_t r = blockIdx.x; r < A.b; r += gridDim.x) {
-        Draw d = A.draw[r];
-        const Rows R = rows_of(A, r);
-        int64_t token = -1;
-        if (drawable(d)) {
-            double* chunk = A.chunk + r * A.chunks;
-            double total = 0.0;
-            for (int pass = 0; pass < 2; ++pass) {
-                total = 0.0;
-                for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
-                    double here;
-                    block_scan(k0 + tid < A.chunks ? chunk[k0 + tid] : 0.0, lds, here);
-                    total += here;
-                }
-                if (total > 0.0 || pass == 1) break;
-                // nothing is left of p (q holds all of it): the draw is from p itself
-                d.with_q = 0;
-                d.out = -1;
-                __syncthreads();
-                for (int k = wave; k < A.chunks; k += kBlock / 64) {
-                    const double sum = chunk_sum<T>(A, d, k, lane);
-                    if (lane == 0) chunk[k] = sum;
-                }
-                __syncthreads();
-            }
-            if (total > 0.0) {
-                const double mark = (double)fminf(fmaxf(A.u_sample[r], 0.0f), 1.0f) * total;
-                // the first chunk whose sum with those before exceeds the mark (at the end: the last that has a sum)
-                if (tid == 0) found = INT_MAX, last = -1;
-                double before = 0.0;
-                for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
-                    const int k = k0 + tid;
-                    const double mine = k < A.chunks ? chunk[k] : 0.0;
-                    double here;
-                    const double upto = before + block_scan(mine, lds, here);
-                    if (mine > 0.0) {
-                        atomicMax(&last, k);
-                        if (upto > mark) atomicMin(&found, k);
-                    }
-                    before += here;
-                    __syncthreads();
-                    if (found != INT_MAX) break;
-                }
-                __syncthreads();
-                const int at = found != INT_MAX ? found : last;
-                // the sum before it, in the same order
-                double prior = 0.0;
-                for (int k0 = 0; k0 <= at; k0 += kBlock) {
-                    double here;
-                    block_scan(k0 + tid < at ? chunk[k0 + tid] : 0.0, lds, here);
-                    prior += here;
-                }
-                __syncthreads();
-                if (tid == 0) found = INT_MAX, last = -1;
-                const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
-                const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
-                const int j0 = at * kVfChunk + tid * kPer;
-                double w[kPer], mine = 0.0;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const int j = j0 + e;
-                    w[e] = j < A.m ? weight<T>(A, d, T::to(s[j]), T::to(q[j]), j) : 0.0;
-                    mine += w[e];
-                }
-                double here;
-                double run = prior + (block_scan(mine, lds, here) - mine);
-                int first = INT_MAX, possible = -1;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    run += w[e];
-                    if (w[e] > 0.0) {
-                        possible = j0 + e;
-                        if (run > mark && first == INT_MAX) first = j0 + e;
-                    }
-                }
-                if (possible >= 0) atomicMax(&last, possible);
-                if (first != INT_MAX) atomicMin(&found, first);
-                __syncthreads();
-                token = found != INT_MAX ? found : last;  // (roundings: the last possible entry of the chunk)
-            }
+    constexpr int kPer = kVfChunkMost / kBlock;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+    double* chunk = A.chunk + r * A.chunks;
+    double total = 0.0;
+    for (int pass = 0; pass < 2; ++pass) {
+        total = 0.0;
+        for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
+            double here;
+            block_scan(k0 + tid < A.chunks ? chunk[k0 + tid] : 0.0, L.scan, here);
+            total += here;
         }
-        const int64_t stop = d.row >= 0 ? d.row : R.hi;
-        bool ended = false;
-        for (int64_t i0 = R.lo; i0 < R.hi; i0 += kBlock) {
-            const int64_t i = i0 + tid;
-            // rows behind one without a drafted token take no part
-            const int64_t drafted = i < R.hi ? A.tokens[i] : 0;
-            const bool none = i < R.hi && drafted < 0;
-            const uint64_t mask = __ballot(none);
-            __syncthreads();
-            if (tid == 0) found = INT_MAX;
-            __syncthreads();
-            if (mask && lane == 0) atomicMin(&found, wave * 64 + __ffsll((unsigned long long)mask) - 1);
-            __syncthreads();
-            const int first_none = found;
-            if (i < R.hi) {
-                const bool in = !ended && tid <= first_none;
-                const int64_t emitted = i < stop ? drafted : i == stop ? token : -1;
-                float ratio = 0.0f, logp = 0.0f;
-                if (in) {
-                    const RowLog p = row_log(A, i, 0);
-                    if (!none) {
-                        RowLog q{0.0, 0.0};
-                        if (A.q) q = row_log(A, i, 1);
-                        ratio = (float)ratio_of<T>(A, i, drafted, p, q);
-                    }
-                    if (emitted >= 0)
-                        logp = (float)(column_log<T>(A.s, A.ld, i, emitted, A.c, p) * 0.6931471805599453094);
-                }
-                A.out_tokens[i] = emitted;
-                A.ratio[i] = ratio;
-                A.logp[i] = logp;
-            }
-            ended = ended || first_none != INT_MAX;
-        }
-        if (tid == 0) {
-            A.accepted[r] = (int32_t)(stop - R.lo);
-            A.next[r] = token;
+        if (total > 0.0 || pass == 1) break;
+        // nothing is left of p (q holds all of it): the draw is from p itself
+        d.with_q = 0;
+        d.out = -1;
+        __syncthreads();
+        for (int k = wave; k < A.chunks; k += kBlock / 64) {
+            const double sum = chunk_sum<T>(A, d, k, lane);
+            if (lane == 0) chunk[k] = sum;
         }
         __syncthreads();
+    }
+    if (tid == 0) A.out_tokens[d.row] = -1;  // (until the draw)
+    if (!(total > 0.0)) return;
+    // the first chunk whose sum with those before exceeds the mark; where roundings leave none, the last with a sum
+    const double mark = (double)fminf(fmaxf(A.u_sample[r], 0.0f), 1.0f) * total;
+    int at = -1;
+    double before = 0.0;
+    for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
+        const int k = k0 + tid;
+        const double mine = k < A.chunks ? chunk[k] : 0.0;
+        double here;
+        const double upto = before + block_scan(mine, L.scan, here);
+        bool found;
+        const int hit = first_over(mine > 0.0 && upto > mark, mine > 0.0, L, found);
+        if (hit >= 0) at = k0 + hit;
+        if (tid == hit) L.prior = upto - mine;
+        before += here;
+        if (found) break;
+    }
+    __syncthreads();
+    const double prior = L.prior;
+    // inside it, each thread some neighbouring entries
+    const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
+    const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
+    const int j0 = at * A.chunk_len + tid * kPer, end = min(A.m, (at + 1) * A.chunk_len);
+    double w[kPer], mine = 0.0;
+    E a[kPer], b[kPer];
+    if (j0 + kPer <= end) {
+        __builtin_memcpy(a, s + j0, sizeof(a));
+        __builtin_memcpy(b, q + j0, sizeof(b));
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            a[e] = s[min(j0 + e, end - 1)];
+            b[e] = q[min(j0 + e, end - 1)];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) w[e] = 0.0;
+    if (j0 < end) {  // (a short chunk leaves waves without)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) w[e] = j0 + e < end ? weight<T>(A, d, T::to(a[e]), T::to(b[e]), j0 + e) : 0.0;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) mine += w[e];
+    double here;
+    double run = prior + (block_scan(mine, L.scan, here) - mine);
+    int first = -1, possible = -1;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        run += w[e];
+        if (w[e] > 0.0) {
+            possible = j0 + e;
+            if (run > mark && first < 0) first = j0 + e;
+        }
+    }
+    bool found;
+    const int hit = first_over(first >= 0, possible >= 0, L, found);
+    if (tid == hit) {
+        const int token = found ? first : possible;  // (roundings: the last possible entry of the chunk)
+        A.next[r] = token;
+        A.out_tokens[d.row] = token;
+        A.logp[d.row] = (float)(column_log(T::to(s[token]), A.c, {d.ref_p, d.log_p}) * 0.6931471805599453094);
+    }
+    __syncthreads();
+}
+
+// Where each request stops and the sums of the chunks of what it draws from: a wave per chunk, A.parts workgroups per
+// request; one that has all the chunks draws too.
+template <class T>
+__global__ __launch_bounds__(kBlock) void k_verify_chunks(VfArgs A) {
+    __shared__ Look L;
+    __shared__ Pick P;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    for (int64_t item = blockIdx.x; item < A.b * A.parts; item += gridDim.x) {
+        const int64_t r = item / A.parts;
+        const int part = (int)(item % A.parts);
+        const Draw d = look<T>(A, r, part == 0, L);
+        if (A.parts > 1 && part == 0 && threadIdx.x == 0) A.draw[r] = d;
+        if (drawable(d))
+            for (int k = part * (kBlock / 64) + wave; k < A.chunks; k += A.parts * (kBlock / 64)) {
+                const double sum = chunk_sum<T>(A, d, k, lane);
+                if (lane == 0) A.chunk[r * A.chunks + k] = sum;
+            }
+        if (A.parts > 1) continue;
+        __syncthreads();
+        if (drawable(d))
+            draw<T>(A, r, d, P);
+        else if (d.row >= 0 && threadIdx.x == 0)
+            A.out_tokens[d.row] = -1;
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(kBlock) void k_verify_draw(VfArgs A) {
+    __shared__ Pick P;
+    for (int64_t r = blockIdx.x; r < A.b; r += gridDim.x) {
+        const Draw d = A.draw[r];
+        if (drawable(d))
+            draw<T>(A, r, d, P);
+        else if (d.row >= 0 && threadIdx.x == 0)
+            A.out_tokens[d.row] = -1;
     }
 }
 
@@ -498,13 +545,9 @@ __global__ __launch_bounds__(kBlock) void k_verify_best(VfArgs A) {
     const int t = threadIdx.x % kThreads, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
     uint64_t* best_of = reinterpret_cast<uint64_t*>(A.sums);
-    const int64_t items = A.n * A.splits;
-    for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items; item0 += (int64_t)gridDim.x * kRows) {
-        const int64_t item = item0 + slot;
-        if (item >= items) return;
-        const int64_t i = item / A.splits;
-        const int split = (int)(item % A.splits);
-        if (!row_counts(A, i, lane)) continue;
+    const int split = (int)blockIdx.y;
+    for (int64_t i = (int64_t)blockIdx.x * kRows + slot; i < A.n; i += (int64_t)gridDim.x * kRows) {
+        if (!row_counts(A, i, false, lane)) continue;
         const E* row = static_cast<const E*>(A.s) + i * A.ld;
         const int runs = A.m / VE, tail = A.m - runs * VE;
         const int v0 = split * A.cut, v1 = min(runs, v0 + A.cut);
@@ -600,18 +643,20 @@ __global__ __launch_bounds__(kBlock) void k_verify_greedy(VfArgs A) {
 
 // ----- host side ------------------------------------------------------------------------
 struct VfPlan {
-    int splits, cut, chunks, parts;
+    int splits, cut, chunk_len, chunks, parts;
     size_t sums, chunk, draw, total;
 };
 
-VfPlan vf_plan(int es, int64_t n, int64_t m, int64_t b) {
+VfPlan vf_plan(int es, int64_t n, int64_t m, int64_t b) {  // (the same with and without draft scores)
     VfPlan P{};
     const int64_t runs = std::max<int64_t>(1, m * es / 16);
     const int64_t most = std::max<int64_t>(1, std::min((kVfFill + n - 1) / std::max<int64_t>(n, 1), runs / kVfCutMin));
     const int64_t cut = (runs + most - 1) / most;
     P.cut = (int)cut;
     P.splits = (int)((runs + cut - 1) / cut);
-    P.chunks = (int)((m + kVfChunk - 1) / kVfChunk);
+    // shorter chunks where they leave waves idle
+    for (P.chunk_len = 512; P.chunk_len < kVfChunkMost && b * m > (int64_t)P.chunk_len * 4 * kVfFill; P.chunk_len *= 2) {}
+    P.chunks = (int)((m + P.chunk_len - 1) / P.chunk_len);
     const int64_t whole = (P.chunks + 3) / 4;
     P.parts = (int)std::max<int64_t>(1, std::min<int64_t>(whole, (kVfFill + b - 1) / std::max<int64_t>(b, 1)));
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -624,30 +669,29 @@ VfPlan vf_plan(int es, int64_t n, int64_t m, int64_t b) {
 template <class T>
 hipError_t verify(const VfArgs& A, bool greedy, hipStream_t s) {
     const bool wave = A.m / Run16<T>::n <= 2 * 64 * kVfVecs;  // such a row, of two blocks at most, is one wave's
-    const int kinds = A.q && !greedy ? 2 : 1, rows = wave ? kBlock / 64 : 1;
-    const int64_t items = A.n * A.splits * kinds;
-    const unsigned grid = (unsigned)std::min<int64_t>((items + rows - 1) / rows, kVfGrid);
+    const int kinds = A.q ? 2 : 1, rows = wave ? kBlock / 64 : 1;
+    const dim3 grid((unsigned)std::min<int64_t>((A.n + rows - 1) / rows, kVfGrid), (unsigned)(A.splits * kinds));
     hipError_t e;
     if (greedy) {
-        if (items == 0)
+        if (A.n == 0)
             ;
         else if (wave)
-            hipLaunchKernelGGL((k_verify_best<T, 1>), dim3(grid), dim3(kBlock), 0, s, A);
+            hipLaunchKernelGGL((k_verify_best<T, 1>), grid, dim3(kBlock), 0, s, A);
         else
-            hipLaunchKernelGGL((k_verify_best<T, 4>), dim3(grid), dim3(kBlock), 0, s, A);
+            hipLaunchKernelGGL((k_verify_best<T, 4>), grid, dim3(kBlock), 0, s, A);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         hipLaunchKernelGGL(k_verify_greedy, dim3((unsigned)std::min<int64_t>((A.b + 3) / 4, kVfGrid)), dim3(kBlock), 0, s, A);
         return hipGetLastError();
     }
-    if (items == 0)
+    if (A.n == 0)
         ;
     else if (wave)
-        hipLaunchKernelGGL((k_verify_sums<T, 1>), dim3(grid), dim3(kBlock), 0, s, A, kinds);
+        hipLaunchKernelGGL((k_verify_sums<T, 1>), grid, dim3(kBlock), 0, s, A);
     else
-        hipLaunchKernelGGL((k_verify_sums<T, 4>), dim3(grid), dim3(kBlock), 0, s, A, kinds);
+        hipLaunchKernelGGL((k_verify_sums<T, 4>), grid, dim3(kBlock), 0, s, A);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL((k_verify_chunks<T>), dim3((unsigned)std::min<int64_t>(A.b * A.parts, kVfGrid)), dim3(kBlock), 0, s, A);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = hipGetLastError()) != hipSuccess || A.parts == 1) return e;
     hipLaunchKernelGGL((k_verify_draw<T>), dim3((unsigned)std::min<int64_t>(A.b, kVfGrid)), dim3(kBlock), 0, s, A);
     return hipGetLastError();
 }
@@ -706,6 +750,9 @@ int sk_scores_verify(const void* scores, int32_t dtype, int64_t n, int64_t m, in
     A.logp = logp;
     A.splits = P.splits;
     A.cut = P.cut;
+    A.width = 1;
+    while (A.width < 64 && A.width < P.splits) A.width *= 2;
+    A.chunk_len = P.chunk_len;
     A.chunks = P.chunks;
     A.parts = P.parts;
     A.sums = reinterpret_cast<Sum*>(base + P.sums);
