@@ -593,9 +593,10 @@ int sk_scores_logprobs_grad(const void *scores, int32_t dtype, int64_t n, int64_
  * Rows of no request are left as they are.  out_tokens may be tokens.  A drafted token
  * >= m is not taken; a masked one (p = 0) neither; one with q = 0 < p is.  A row that the
  * mask leaves empty takes nothing and draws nothing (-1).  A NaN or +inf score, of the draft
- * too, makes its row's ratio NaN (not taken) and nothing is drawn there.  Exponentials, sums
- * and comparisons are float64 and probabilities below 2^-1000 count as 0, so decisions and
- * draws are those of the exact probabilities but within some 2^-45 of a border.
+ * too, makes its row's ratio NaN (not taken) and nothing is drawn there.  ratio and logp
+ * come from float32 sums; a decision that these leave open, and every draw, is taken in
+ * float64 (probabilities below 2^-1000 count as 0), so that they are those of the exact
+ * probabilities but within some 2^-38 of a border.
  */
 size_t sk_scores_verify_workspace_bytes(int32_t dtype, int64_t n, int64_t m, int64_t b);
 int sk_scores_verify(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,

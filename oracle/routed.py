@@ -109,7 +109,7 @@ def verify(scores, tokens, starts, u_accept, u_sample, draft=None, eps=1.0, eps_
                     q[t] = 1.0
                 pt, qt = (p[t], q[t]) if t < m else (0.0, 1.0)
                 ratio[i] = np.nan if bad else 0.0 if pt == 0.0 else 1.0 if pt >= qt else pt / qt
-                taken = ratio[i] > 0.0 and (eps == 0.0 or u_accept[i] < ratio[i])
+                taken = ratio[i] > 0.0 and (eps == 0.0 or float(u_accept[i]) * qt < pt)
             ended = t < 0
             if stopped:
                 continue

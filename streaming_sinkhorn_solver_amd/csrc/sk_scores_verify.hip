@@ -7,10 +7,17 @@
 // the residual max(p - q, 0).  That pair of draws is the maximal coupling of q and
 // p, the transport plan of least cost 1[x != y].
 //
-// A decision or a draw next to a border must not depend on how sums are taken, so
-// exponentials and sums are in float64 throughout: the error of a probability is
-// some 2^-38 of it, where a row of 131072 has borders 2^-17 apart in the mean and the
-// random numbers are multiples of 2^-24.
+// A decision or a draw next to a border must not depend on how sums are taken.  All
+// rows' sums are taken in float32, at the rate that the scores arrive; a decision that
+// lies within the bound of their error (some 2^-15 of p / q) takes its row's sums again
+// in float64.  What is drawn from, one row per request, goes in float64 throughout: the
+// error of a probability is some 2^-38 of it, where a row of 131072 has borders 2^-17
+// apart in the mean and the random numbers are multiples of 2^-24.  With e and h the
+// exponentials of p's and q's row and rho the quotient of their sums, the residual is
+// max(e - rho h, 0).  One pass takes sum e and sum h, which give rho, and with rho0 from the
+// float32 sums R = sum max(e - rho0 h, 0) and B = sum of h where e > rho0 h.  The residual's
+// sum is then R + (rho0 - rho) B but for entries between the two quotients, which are off by
+// their distance 2^-20 and a share of 2^-20 of all.
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -26,8 +33,8 @@ constexpr int kVfFill = 1024, kVfCutMin = 1024;
 constexpr double kFloor = -1000.0;    // exponents below count as zero
 constexpr double kUnset = -1.0e300;   // reference of a part without an unmasked entry
 
-// What is needed of a row, or a part of one: sum of 2^(c (s - ref)); NaN if a score is NaN or +inf.  The reference is a
-// score, and the difference to it is taken first: rows of a type's lowest value lose nothing.
+// What is needed of a row, or a part of one: sum of 2^(c (s - ref)), NaN if a score is NaN or +inf.  The reference is the
+// largest score, and the difference to it is taken first: rows of a type's lowest value lose nothing.
 struct Sum {
     double ref, s;
 };
@@ -35,7 +42,7 @@ struct Sum {
 // What a request's draw needs.
 struct Draw {
     double ref_p, log_p;  // reference of the row's sum, and the sum's log2
-    double ref_q, log_q;  // of the draft's row
+    double ref_q, rho;    // of the draft's row; the quotient of the two sums
     int64_t row;          // where the request stops, -1: nothing is drawn
     int64_t out;          // column that the residual leaves out, or -1
     int64_t with_q;
@@ -45,7 +52,9 @@ struct VfArgs {
     const void *s, *q;
     int64_t ld, ldq, n, b;
     int m;
-    double c, cq;  // log2e / eps
+    double c, cq;    // log2e / eps
+    float cf, cqf;   // the same in float32
+    double doubt;    // relative error of p / q from the float32 sums at most
     const int64_t *tokens, *starts;
     const float *u_accept, *u_sample;
     int32_t* accepted;
@@ -55,7 +64,7 @@ struct VfArgs {
     int width;        // lanes that join a row's parts: a power of two
     int chunk_len, chunks, parts;
     Sum* sums;        // [n][2][splits]
-    double* chunk;    // [b][chunks]
+    double* chunk;    // [b][chunks][4]
     Draw* draw;       // [b]
 };
 
@@ -102,13 +111,6 @@ __device__ __forceinline__ Sum join(Sum a, Sum b, double c) {
     const double ref = fmax(a.ref, b.ref);
     return {ref, moved(a, ref, c) + moved(b, ref, c)};
 }
-template <int L>
-__device__ __forceinline__ Sum lanes_join(Sum a, double c) {
-    double ref = a.ref;
-    for (int o = 1; o < L; o *= 2) ref = fmax(ref, __shfl_xor(ref, o));
-    return {ref, lanes_sum<L>(moved(a, ref, c))};
-}
-
 // Whether row i of the target (of the draft) is one that a request looks at.  All lanes of a wave, i the same in each.
 __device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draft, int lane) {
     const int64_t lowest = A.starts[0], end = A.starts[A.b], here = A.tokens[i], before = A.tokens[i > 0 ? i - 1 : 0];
@@ -128,20 +130,24 @@ __device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draf
     return __ballot(lane < size && A.starts[min(lo + lane, A.b)] == i) != 0;
 }
 
-// Sums of the rows' exponentials: a row, or a part of one, per W waves.
+// S for the reference M to the same for top >= M.
+__device__ __forceinline__ float rescaled(float S, float M, float top, float c) { return S * s_ex2((M - top) * c); }
+
+// Sums of the rows' exponentials in float32: a row, or a part of one, per W waves, each thread with a running maximum
+// that it moves once per kVfVecs loads.  (A NaN or +inf score makes the sum NaN by itself.)
 template <class T, int W>
 __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
     using E = typename T::type;
     constexpr int VE = Run16<T>::n, kThreads = W * 64, kRows = kBlock / kThreads, NV = kVfVecs, kStep = kThreads * NV;
-    __shared__ Sum red[kBlock / 64];
+    __shared__ float red[kBlock / 64][2];
     const int t = threadIdx.x % kThreads, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
     // the grid's second dimension: parts of a row, of the target's and then of the draft's
     const int kind = blockIdx.y >= (unsigned)A.splits, split = (int)blockIdx.y - kind * A.splits;
     const bool draft = kind == 1;
+    const float c = draft ? A.cqf : A.cf;
     for (int64_t i = (int64_t)blockIdx.x * kRows + slot; i < A.n; i += (int64_t)gridDim.x * kRows) {
         const E* row = static_cast<const E*>(draft ? A.q : A.s) + i * (draft ? A.ldq : A.ld);
-        const double c = draft ? A.cq : A.c;
         const int runs = A.m / VE, tail = A.m - runs * VE;
         const int v0 = split * A.cut, v1 = min(runs, v0 + A.cut);
         const int blocks = v1 > v0 ? (v1 - v0 + kStep - 1) / kStep : 0;
@@ -152,22 +158,11 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
         };
         if (blocks > 0) fetch(0);  // (before it is known whether the row counts)
         if (!row_counts(A, i, draft, lane)) continue;
-        double ref = 0.0, S = 0.0;
-        const double floor = kFloor / c;
-        float limit = -INFINITY;  // a larger score moves the reference
-        bool set = false, bad = false;
-        auto raise = [&](float top) {
-            if (!(top < INFINITY)) bad = true;  // NaN or +inf
-            if (!(top > limit) || bad) return;
-            S = set ? moved({ref, S}, top, c) : 0.0;
-            ref = top;
-            limit = (float)(ref + 400.0 / c);
-            set = true;
-        };
+        float M = kNegBig, S = 0.0f;  // (M starts above -inf)
         if (split == 0 && t < tail) {
             const float x = T::to(row[runs * VE + t]);
-            raise(x);
-            if (set) S += pow2_or_zero(((double)x - ref) * c);
+            M = fmaxf(M, x);
+            S = s_ex2((x - M) * c);
         }
         for (int b = 0; b < blocks; ++b) {
 #pragma unroll
@@ -177,37 +172,39 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
             } else {
 #pragma unroll
                 for (int q = 0; q < NV; ++q)
-                    if (v0 + b * kStep + q * kThreads + t >= v1)
-                        v[q].fill(T::kNegInfBits);
+                    if (v0 + b * kStep + q * kThreads + t >= v1) v[q].fill(T::kNegInfBits);
             }
-            float top = v[0].at(0);
+            float top = M;
 #pragma unroll
             for (int q = 0; q < NV; ++q)
 #pragma unroll
-                for (int e = 0; e < VE; ++e) top = __builtin_elementwise_maximum(top, v[q].at(e));  // (keeps a NaN)
-            raise(top);
-            double s0 = 0.0, s1 = 0.0;
+                for (int e = 0; e < VE; ++e) top = fmaxf(top, v[q].at(e));
+            S = rescaled(S, M, top, c);
+            M = top;
+            float s = 0.0f;
 #pragma unroll
             for (int q = 0; q < NV; ++q)
 #pragma unroll
-                for (int e = 0; e < VE; e += 2) {
-                    // (a masked score's 2^-1000 is lost against the 1 of the reference)
-                    s0 += pow2(fmax((double)v[q].at(e) - ref, floor), c);
-                    s1 += pow2(fmax((double)v[q].at(e + 1) - ref, floor), c);
-                }
-            S += s0 + s1;
+                for (int e = 0; e < VE; ++e) s += s_ex2((v[q].at(e) - M) * c);
+            S += s;
         }
-        Sum sum{set ? ref : kUnset, bad ? (double)NAN : set ? S : 0.0};
-        sum = lanes_join<64>(sum, c);
+        float top = lanes_max<64>(M);
         if (W > 1) {
             __syncthreads();
-            if (lane == 0) red[wave] = sum;
+            if (lane == 0) red[wave][0] = top;
             __syncthreads();
-            sum = red[0];
 #pragma unroll
-            for (int w = 1; w < W; ++w) sum = join(sum, red[w], c);
+            for (int w = 0; w < W; ++w) top = fmaxf(top, red[w][0]);
         }
-        if (t == 0) A.sums[(i * 2 + kind) * A.splits + split] = sum;
+        S = lanes_sum<64>(rescaled(S, M, top, c));
+        if (W > 1) {
+            if (lane == 0) red[wave][1] = S;
+            __syncthreads();
+            S = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) S += red[w][1];
+        }
+        if (t == 0) A.sums[(i * 2 + kind) * A.splits + split] = {(double)top, (double)S};
     }
 }
 
@@ -231,8 +228,36 @@ __device__ __forceinline__ Rows rows_of(const VfArgs& A, int64_t r) {
 struct Look {
     RowLog row[2][64];
     Draw draw;
-    int stop, none;  // in a block of 64 rows: the first that is not taken, that has no drafted token; 64: not there
+    double part[kBlock / 64];
+    int stop, none, again;  // in a block of 64 rows: the first that is not taken, that has no drafted token (64: not
+                            // there); one to be summed again (-1: none)
 };
+
+// A row's log2 sum in float64, by a whole workgroup; ref is the row's largest score.
+template <class T>
+__device__ double exact_log(const void* m, int64_t ld, int64_t i, int cols, double c, double ref, double* part) {
+    using E = typename T::type;
+    constexpr int VE = Run16<T>::n;
+    const E* row = static_cast<const E*>(m) + i * ld;
+    double sum = 0.0;
+    Run16<T> v;
+#pragma unroll 1
+    for (int q = threadIdx.x; q < cols / VE; q += kBlock) {
+        v.get(row + (int64_t)q * VE);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) sum += pow2_or_zero(((double)v.at(e) - ref) * c);
+    }
+    const int j = cols / VE * VE + threadIdx.x;
+    if (j < cols) sum += pow2_or_zero(((double)T::to(row[j]) - ref) * c);
+    sum = lanes_sum<64>(sum);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kBlock / 64; ++w) sum += part[w];
+    return log2_of(sum);
+}
 
 // Where a request stops, by a whole workgroup: the first row whose token is not taken or that has none.  64 rows at a
 // time: A.width lanes join the parts of a row's sum, then a wave has a row per lane.  With write, the request's outputs
@@ -271,33 +296,54 @@ __device__ Draw look(const VfArgs& A, int64_t r, bool write, Look& L) {
             for (int o = 1; o < A.width; o *= 2) all += __shfl_xor(all, o);
             if (part == 0) L.row[kind][row] = {ref, all == 0.0 ? -(double)INFINITY : all != all ? all : log2_of(all)};
         }
-        __syncthreads();
-        if (wave == 0) {
-            const RowLog P = L.row[0][lane], Q = L.row[A.q ? 1 : 0][lane];
-            const double lp = known ? column_log(s, A.c, P) : P.log_sum == P.log_sum ? -(double)INFINITY : P.log_sum;
-            const double lq = !A.q ? 0.0 : known ? column_log(q, A.cq, Q) : Q.log_sum;
-            // p(x) / q(x), at most 1; NaN where one of the rows holds a NaN or +inf
-            const double gap = lp - lq;
-            const double ratio = lp != lp || lq != lq ? (double)NAN
-                                 : lp < kFloor        ? 0.0
-                                 : gap >= 0.0 || lq < kFloor ? 1.0
-                                                             : pow2_or_zero(gap);
-            const bool taken = token >= 0 && (double)u < ratio && ratio > 0.0;
-            const uint64_t stops = __ballot(on && !taken), nones = __ballot(on && token < 0);
-            const int stop = stops ? __ffsll((unsigned long long)stops) - 1 : 64;
-            const int none = nones ? __ffsll((unsigned long long)nones) - 1 : 64;
-            if (lane == stop)
-                L.draw = {P.ref, P.log_sum, Q.ref, Q.log_sum, i, A.q || !known ? -1 : token, A.q && token >= 0};
-            if (lane == 0) L.stop = stop, L.none = none;
-            if (write && on) {
-                const bool emits = !stopped && lane < stop;
-                if (stopped || lane > stop) A.out_tokens[i] = -1;
-                if (emits) A.out_tokens[i] = token;
-                A.ratio[i] = ended || lane >= none ? 0.0f : (float)ratio;
-                A.logp[i] = emits ? (float)(lp * 0.6931471805599453094) : 0.0f;
+        uint64_t exact = 0;  // rows whose sums were taken again
+        for (int tries = 0; tries <= 64; ++tries) {  // (each row is summed again once at most)
+            __syncthreads();
+            if (wave == 0) {
+                const RowLog P = L.row[0][lane], Q = L.row[A.q ? 1 : 0][lane];
+                const double lp = known ? column_log(s, A.c, P) : P.log_sum == P.log_sum ? -(double)INFINITY : P.log_sum;
+                const double lq = !A.q ? 0.0 : known ? column_log(q, A.cq, Q) : Q.log_sum;
+                // p(x) / q(x), at most 2; NaN where one of the rows holds a NaN or +inf
+                const double quotient = lp != lp || lq != lq ? (double)NAN
+                                        : lp < kFloor        ? 0.0
+                                        : lq < kFloor        ? 2.0
+                                                             : pow2_or_zero(fmin(lp - lq, 1.0));
+                const bool taken = token >= 0 && (double)u < quotient && quotient > 0.0;
+                const bool near = token >= 0 && !(exact >> lane & 1) && quotient > 0.0 &&
+                                  fabs((double)u - quotient) <= A.doubt * quotient;
+                const uint64_t stops = __ballot(on && !taken), nears = __ballot(on && near), nones = __ballot(on && token < 0);
+                const int stop = stops ? __ffsll((unsigned long long)stops) - 1 : 64;
+                const int none = nones ? __ffsll((unsigned long long)nones) - 1 : 64;
+                const int first_near = nears ? __ffsll((unsigned long long)nears) - 1 : 64;
+                const int again = !stopped && nears && first_near <= stop ? first_near : -1;
+                if (lane == 0) L.again = again;
+                if (again < 0) {
+                    if (lane == stop) {
+                        const bool with_q = A.q && token >= 0 && !(Q.log_sum == -(double)INFINITY);
+                        const double gap = P.log_sum - Q.log_sum;  // (of sums from 1 to m, where there is something to draw)
+                        const double rho = !with_q ? 0.0 : gap == gap ? pow2(fmin(fmax(gap, -64.0), 64.0), 1.0) : gap;
+                        L.draw = {P.ref, P.log_sum, Q.ref, rho, i, A.q || !known ? -1 : token, with_q};
+                    }
+                    if (lane == 0) L.stop = stop, L.none = none;
+                    if (write && on) {
+                        const bool emits = !stopped && lane < stop;
+                        if (stopped || lane > stop) A.out_tokens[i] = -1;
+                        if (emits) A.out_tokens[i] = token;
+                        A.ratio[i] = ended || lane >= none ? 0.0f : quotient > 1.0 ? 1.0f : (float)quotient;
+                        A.logp[i] = emits ? (float)(lp * 0.6931471805599453094) : 0.0f;
+                    }
+                }
+            }
+            __syncthreads();
+            const int row = L.again;
+            if (row < 0) break;
+            exact |= 1ull << row;
+            for (int kind = 0; kind < kinds; ++kind) {
+                const double ref = L.row[kind][row].ref;
+                const double log_sum = exact_log<T>(kind ? A.q : A.s, kind ? A.ldq : A.ld, i0 + row, A.m, kind ? A.cq : A.c, ref, L.part);
+                if (tid == 0 && L.row[kind][row].log_sum > -(double)INFINITY) L.row[kind][row].log_sum = log_sum;
             }
         }
-        __syncthreads();
         if (!stopped && L.stop < 64) {
             d = L.draw;
             stopped = true;
@@ -313,31 +359,38 @@ __device__ Draw look(const VfArgs& A, int64_t r, bool write, Look& L) {
     return d;
 }
 
-// An entry of what is drawn from: max(p - q, 0), or, where no draft scores take part, p relative to its reference.
-// (An exponent that is NaN, that of a draft row without an unmasked entry, counts as zero too.)
-template <class T>
-__device__ __forceinline__ double weight(const VfArgs& A, const Draw& d, float s, float t, int64_t j) {
-    if (d.with_q) {
-        const double p = pow2_or_zero(fma((double)s - d.ref_p, A.c, -d.log_p));
-        const double q = pow2_or_zero(fma((double)t - d.ref_q, A.cq, -d.log_q));
-        return fmax(p - q, 0.0);
-    }
-    return j == d.out ? 0.0 : pow2_or_zero(((double)s - d.ref_p) * A.c);
-}
 __device__ __forceinline__ bool drawable(const Draw& d) {
-    const bool p = d.log_p > -(double)INFINITY;  // (NaN: no)
-    return d.row >= 0 && p && (!d.with_q || d.log_q == d.log_q);
+    return d.row >= 0 && d.log_p > -(double)INFINITY && (!d.with_q || d.rho == d.rho);  // (NaN: no)
 }
 
-// Sum of a chunk's weights, by all lanes of a wave, the same in each.
+// An entry's exponentials: p's, 0 in the column that is left out, and q's.
+struct Pair {
+    double e, h;
+};
+__device__ __forceinline__ Pair pair_of(const VfArgs& A, const Draw& d, float s, float t, int64_t j) {
+    const double e = pow2_or_zero(((double)s - d.ref_p) * A.c);
+    return {j == d.out ? 0.0 : e, d.with_q ? pow2_or_zero(((double)t - d.ref_q) * A.cq) : 0.0};
+}
+
+// Sums over a chunk, by a wave: of e, of h, of max(e - rho h, 0) and of h where that is positive (without q: of e).
 template <class T>
-__device__ __forceinline__ double chunk_sum(const VfArgs& A, const Draw& d, int chunk, int lane) {
+__device__ __forceinline__ void chunk_sums(const VfArgs& A, const Draw& d, int chunk, int lane, double* out) {
     using E = typename T::type;
     constexpr int VE = Run16<T>::n;
     const int start = chunk * A.chunk_len, j0 = start + lane * VE, size = min(A.chunk_len, A.m - start);
     const E* s = static_cast<const E*>(A.s) + d.row * A.ld + j0;
     const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld) + j0;
-    double sum = 0.0;
+    double e = 0.0, h = 0.0, rest = 0.0, hot = 0.0;
+    auto add = [&](float x, float y, int j) {
+        const Pair p = pair_of(A, d, x, y, j);
+        const double w = fma(-d.rho, p.h, p.e);
+        e += p.e;
+        if (d.with_q) {
+            h += p.h;
+            rest += fmax(w, 0.0);
+            hot += w > 0.0 ? p.h : 0.0;
+        }
+    };
     if (size == A.chunk_len) {
         Run16<T> a, b, a1, b1;
         a1.get(s);
@@ -350,16 +403,28 @@ __device__ __forceinline__ double chunk_sum(const VfArgs& A, const Draw& d, int 
             a1.get(s + next);
             b1.get(q + next);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) sum += weight<T>(A, d, a.at(e), b.at(e), j0 + at + e);
+            for (int c = 0; c < VE; ++c) add(a.at(c), b.at(c), j0 + at + c);
         }
     } else {
 #pragma unroll 1
         for (int at = 0; at < size; at += 64 * VE)
 #pragma unroll 1
-            for (int e = 0; e < VE && at + lane * VE + e < size; ++e)
-                sum += weight<T>(A, d, T::to(s[at + e]), T::to(q[at + e]), j0 + at + e);
+            for (int c = 0; c < VE && at + lane * VE + c < size; ++c) add(T::to(s[at + c]), T::to(q[at + c]), j0 + at + c);
     }
-    return lanes_sum<64>(sum);
+    if (!d.with_q) {
+        e = lanes_sum<64>(e);
+        if (lane == 0) out[0] = e;
+        return;
+    }
+    // four sums over the lanes at once: half of the lanes take two of them, a quarter one each
+    const bool high = lane & 32, odd = lane & 16;
+    double x0 = high ? rest : e, x1 = high ? hot : h;
+    x0 += __shfl_xor(high ? e : rest, 32);
+    x1 += __shfl_xor(high ? h : hot, 32);
+    double x = odd ? x1 : x0;
+    x += __shfl_xor(odd ? x0 : x1, 16);
+    for (int o = 8; o > 0; o /= 2) x += __shfl_xor(x, o);
+    if ((lane & 15) == 0) out[lane / 16] = x;
 }
 
 // Inclusive sums over the workgroup's threads; the last is the same in every thread.
@@ -410,44 +475,64 @@ template <class T>
 __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
     using E = typename T::type;
     constexpr int kPer = kVfChunkMost / kBlock;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
-    double* chunk = A.chunk + r * A.chunks;
-    double total = 0.0;
-    for (int pass = 0; pass < 2; ++pass) {
-        total = 0.0;
-        for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
-            double here;
-            block_scan(k0 + tid < A.chunks ? chunk[k0 + tid] : 0.0, L.scan, here);
-            total += here;
-        }
-        if (total > 0.0 || pass == 1) break;
-        // nothing is left of p (q holds all of it): the draw is from p itself
-        d.with_q = 0;
-        d.out = -1;
-        __syncthreads();
-        for (int k = wave; k < A.chunks; k += kBlock / 64) {
-            const double sum = chunk_sum<T>(A, d, k, lane);
-            if (lane == 0) chunk[k] = sum;
-        }
-        __syncthreads();
-    }
+    const int tid = threadIdx.x;
+    const double* sums = A.chunk + r * A.chunks * 4;
     if (tid == 0) A.out_tokens[d.row] = -1;  // (until the draw)
-    if (!(total > 0.0)) return;
+    double shift = 0.0, all = 0.0;  // rho0 - rho; the sum of e
+    if (d.with_q) {
+        double h = 0.0;
+        for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
+            const int k = k0 + tid;
+            double here;
+            block_scan(k < A.chunks ? sums[4 * k] : 0.0, L.scan, here);
+            all += here;
+            block_scan(k < A.chunks ? sums[4 * k + 1] : 0.0, L.scan, here);
+            h += here;
+        }
+        shift = d.rho - all / h;
+        d.rho = all / h;
+    }
+    auto weight_of = [&](int k) {
+        if (k >= A.chunks) return 0.0;
+        return d.with_q ? fmax(fma(shift, sums[4 * k + 3], sums[4 * k + 2]), 0.0) : sums[4 * k];
+    };
+    double mine = 0.0, upto = 0.0, here, total = 0.0;
+    for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
+        mine = weight_of(k0 + tid);
+        upto = block_scan(mine, L.scan, here);
+        total += here;
+    }
+    if (d.with_q && !(total > 0x1p-40 * all)) {
+        // p - q leaves nothing (q = p, but for roundings): the draw is from p itself
+        d.with_q = 0;
+        total = all;
+        if (A.chunks <= kBlock) {
+            mine = weight_of(tid);
+            upto = block_scan(mine, L.scan, here);
+        }
+    }
+    if (!(total > 0.0)) {
+        // all of p is at the column left out: that is drawn
+        if (tid == 0 && d.out >= 0) {
+            A.next[r] = A.out_tokens[d.row] = d.out;
+            A.logp[d.row] = 0.0f;
+        }
+        return;
+    }
     // the first chunk whose sum with those before exceeds the mark; where roundings leave none, the last with a sum
     const double mark = (double)fminf(fmaxf(A.u_sample[r], 0.0f), 1.0f) * total;
     int at = -1;
     double before = 0.0;
-    for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
-        const int k = k0 + tid;
-        const double mine = k < A.chunks ? chunk[k] : 0.0;
-        double here;
-        const double upto = before + block_scan(mine, L.scan, here);
-        bool found;
+    bool found = false;
+    for (int k0 = 0; k0 < A.chunks && !found; k0 += kBlock) {
+        if (A.chunks > kBlock) {  // (else both are there)
+            mine = weight_of(k0 + tid);
+            upto = before + block_scan(mine, L.scan, here);
+            before += here;
+        }
         const int hit = first_over(mine > 0.0 && upto > mark, mine > 0.0, L, found);
         if (hit >= 0) at = k0 + hit;
         if (tid == hit) L.prior = upto - mine;
-        before += here;
-        if (found) break;
     }
     __syncthreads();
     const double prior = L.prior;
@@ -455,27 +540,29 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
     const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
     const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
     const int j0 = at * A.chunk_len + tid * kPer, end = min(A.m, (at + 1) * A.chunk_len);
-    double w[kPer], mine = 0.0;
-    E a[kPer], b[kPer];
-    if (j0 + kPer <= end) {
-        __builtin_memcpy(a, s + j0, sizeof(a));
-        __builtin_memcpy(b, q + j0, sizeof(b));
-    } else {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            a[e] = s[min(j0 + e, end - 1)];
-            b[e] = q[min(j0 + e, end - 1)];
-        }
-    }
+    double w[kPer];
+    mine = 0.0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) w[e] = 0.0;
     if (j0 < end) {  // (a short chunk leaves waves without)
+        E a[kPer], b[kPer];
+        if (j0 + kPer <= end) {
+            __builtin_memcpy(a, s + j0, sizeof(a));
+            __builtin_memcpy(b, q + j0, sizeof(b));
+        } else {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) w[e] = j0 + e < end ? weight<T>(A, d, T::to(a[e]), T::to(b[e]), j0 + e) : 0.0;
+            for (int e = 0; e < kPer; ++e) {
+                a[e] = s[min(j0 + e, end - 1)];
+                b[e] = q[min(j0 + e, end - 1)];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const Pair p = pair_of(A, d, T::to(a[e]), T::to(b[e]), j0 + e);
+            w[e] = j0 + e < end ? fmax(fma(-d.rho, p.h, p.e), 0.0) : 0.0;
+            mine += w[e];
+        }
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) mine += w[e];
-    double here;
     double run = prior + (block_scan(mine, L.scan, here) - mine);
     int first = -1, possible = -1;
 #pragma unroll
@@ -486,7 +573,6 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
             if (run > mark && first < 0) first = j0 + e;
         }
     }
-    bool found;
     const int hit = first_over(first >= 0, possible >= 0, L, found);
     if (tid == hit) {
         const int token = found ? first : possible;  // (roundings: the last possible entry of the chunk)
@@ -510,10 +596,8 @@ __global__ __launch_bounds__(kBlock) void k_verify_chunks(VfArgs A) {
         const Draw d = look<T>(A, r, part == 0, L);
         if (A.parts > 1 && part == 0 && threadIdx.x == 0) A.draw[r] = d;
         if (drawable(d))
-            for (int k = part * (kBlock / 64) + wave; k < A.chunks; k += A.parts * (kBlock / 64)) {
-                const double sum = chunk_sum<T>(A, d, k, lane);
-                if (lane == 0) A.chunk[r * A.chunks + k] = sum;
-            }
+            for (int k = part * (kBlock / 64) + wave; k < A.chunks; k += A.parts * (kBlock / 64))
+                chunk_sums<T>(A, d, k, lane, A.chunk + (r * A.chunks + k) * 4);
         if (A.parts > 1) continue;
         __syncthreads();
         if (drawable(d))
@@ -642,6 +726,9 @@ __global__ __launch_bounds__(kBlock) void k_verify_greedy(VfArgs A) {
 }
 
 // ----- host side ------------------------------------------------------------------------
+// A row of two blocks at most is one wave's.
+bool one_wave(int es, int64_t m) { return m / (16 / es) <= 2 * 64 * kVfVecs; }
+
 struct VfPlan {
     int splits, cut, chunk_len, chunks, parts;
     size_t sums, chunk, draw, total;
@@ -661,14 +748,14 @@ VfPlan vf_plan(int es, int64_t n, int64_t m, int64_t b) {  // (the same with and
     P.parts = (int)std::max<int64_t>(1, std::min<int64_t>(whole, (kVfFill + b - 1) / std::max<int64_t>(b, 1)));
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     P.chunk = up((size_t)n * 2 * (size_t)P.splits * sizeof(Sum));
-    P.draw = P.chunk + up((size_t)b * (size_t)P.chunks * sizeof(double));
+    P.draw = P.chunk + up((size_t)b * (size_t)P.chunks * 4 * sizeof(double));
     P.total = P.draw + up((size_t)b * sizeof(Draw)) + 256;
     return P;
 }
 
 template <class T>
 hipError_t verify(const VfArgs& A, bool greedy, hipStream_t s) {
-    const bool wave = A.m / Run16<T>::n <= 2 * 64 * kVfVecs;  // such a row, of two blocks at most, is one wave's
+    const bool wave = one_wave((int)sizeof(typename T::type), A.m);
     const int kinds = A.q ? 2 : 1, rows = wave ? kBlock / 64 : 1;
     const dim3 grid((unsigned)std::min<int64_t>((A.n + rows - 1) / rows, kVfGrid), (unsigned)(A.splits * kinds));
     hipError_t e;
@@ -720,9 +807,9 @@ int sk_scores_verify(const void* scores, int32_t dtype, int64_t n, int64_t m, in
     if (st) return st;
     if (!good_sizes(n, m, b)) return SK_ERR_SHAPE;
     if (draft && (st = check_scores(draft, dtype, n, m, ld_draft))) return st;
-    if (!std::isfinite(eps) || eps < 0.0f) return SK_ERR_EPS;
     const bool greedy = eps == 0.0f;
-    if (draft && (!std::isfinite(eps_draft) || eps_draft <= 0.0f)) return SK_ERR_EPS;
+    if (!greedy && (st = check_temperature(eps))) return st;
+    if (draft && (st = check_temperature(eps_draft))) return st;
     const VfPlan P = vf_plan(elem_size(dtype), n, m, b);
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < P.total) return SK_ERR_WORKSPACE;
     if (b == 0) return SK_OK;
@@ -739,6 +826,13 @@ int sk_scores_verify(const void* scores, int32_t dtype, int64_t n, int64_t m, in
     A.m = (int)m;
     A.c = greedy ? 1.0 : 1.4426950408889634074 / (double)eps;
     A.cq = draft ? 1.4426950408889634074 / (double)eps_draft : 1.0;
+    A.cf = (float)A.c;
+    A.cqf = (float)A.cq;
+    // the float32 sums: an exponent carries 3 u of itself, and as much again by the moves of the maximum, of which the
+    // weighted mean is at most ln m; 2 u the exponential; then the additions of a block, of the blocks (with 3 u for each
+    // move), lanes and waves
+    const int64_t blocks = P.cut / ((one_wave(elem_size(dtype), m) ? 64 : kBlock) * kVfVecs) + 1;
+    A.doubt = 2.5 * (6.0 * std::log((double)m) + 60.0 + 4.0 * (double)blocks) * 0x1p-24;
     A.tokens = tokens;
     A.starts = starts;
     A.u_accept = u_accept;

@@ -43,11 +43,16 @@ def check(got, want, scores, eps):
     assert np.array_equal(got.accepted.cpu().numpy(), accepted)
     assert np.array_equal(got.next.cpu().numpy(), after)
     assert np.array_equal(got.tokens.cpu().numpy(), emitted)
-    # float64 throughout: exponents off by a few 2^-53 of the largest one, sums of at most m terms; one float32 rounding
+    # p and q come from float32 sums: a term carries 3 u of its exponent and as much by the moves of the running maximum
+    # (weighted mean at most ln m) and 2 u of the exponential; then at most 32 additions of a block, 4 u for each of a
+    # thread's blocks (two of them at the least, one per 4096 scores at the most) and 20 u for lanes, waves and parts.
+    # All else is float64: exponents off by some 2^-50 of the largest; one rounding to float32.
+    m = scores.shape[1]
+    one = (6 * np.log(m) + 60 + 4 * (m / 4096 + 2)) * U
     big = np.abs(np.where(np.isfinite(scores), scores, 0.0)).max(initial=1.0) / (eps or 1.0)
     noise = (big + 64) * 2.0 ** -48
-    close(got.ratio, ratio, U * np.abs(ratio) + noise + 2.0 ** -149, "ratio")
-    close(got.logp, logp, U * np.abs(logp) + noise, "logp")
+    close(got.ratio, ratio, (2 * one + U) * np.abs(ratio) + noise + 2.0 ** -149, "ratio")
+    close(got.logp, logp, one + U * np.abs(logp) + noise, "logp")
 
 
 def run(data, ref, eps=1.0, eps_draft=1.0, **how):
@@ -198,6 +203,26 @@ def test_random_numbers_at_their_borders():
             got = sk.scores_verify(s, tokens, starts, a, u, draft=draft)
             rows = got.tokens >= 0
             assert (got.tokens < 64).all() and torch.isfinite(s[rows, got.tokens[rows]]).all()
+
+
+@pytest.mark.parametrize("m", [300, 20000])
+@pytest.mark.parametrize("draft", [True, False])
+def test_decisions_next_to_the_border(m, draft):
+    """u just below and just above p / q: float32 numbers around it, closer than float32 sums can tell."""
+    lengths = [4] * 40
+    data, ref = case(lengths, m, "f32", m, draft)
+    s, q, tokens, starts, ua, us = data
+    ss, qs, t, st, a, u = ref
+    n = len(t)
+    r = np.random.default_rng(7)
+    for i in range(n):
+        if t[i] < 0:
+            continue
+        p = oro.distribution(ss[i], 1.0)[0][t[i]]
+        x = p / oro.distribution(qs[i], 1.0)[0][t[i]] if draft else p
+        v = np.float32(min(x, 1.0))
+        a[i] = np.nextafter(v, np.float32(r.integers(0, 2) * 2)) if r.random() < 0.7 else v
+    run((s, q, tokens, starts, gpu(a), us), (ss, qs, t, st, a, u))
 
 
 def test_tokens_of_no_column():
