@@ -595,7 +595,7 @@ int sk_scores_logprobs_grad(const void *scores, int32_t dtype, int64_t n, int64_
  * mask leaves empty takes nothing and draws nothing (-1).  A NaN or +inf score, of the draft
  * too, makes its row's ratio NaN (not taken) and nothing is drawn there.  ratio and logp
  * come from float32 sums; a decision that these leave open, and every draw, is taken in
- * float64 (probabilities below 2^-1000 count as 0), so that they are those of the exact
+ * float64 (probabilities below 2^-900 count as 0), so that they are those of the exact
  * probabilities but within some 2^-38 of a border.
  */
 size_t sk_scores_verify_workspace_bytes(int32_t dtype, int64_t n, int64_t m, int64_t b);

@@ -30,7 +30,8 @@ constexpr int64_t kVfMaxCols = (int64_t)1 << 30;
 constexpr int kVfVecs = 4;             // 16-byte loads of a thread's block
 constexpr int kVfChunkMost = 2048;    // entries of the residual whose sum is kept: 512, 1024 or 2048
 constexpr int kVfFill = 1024, kVfCutMin = 1024;
-constexpr double kFloor = -1000.0;    // exponents below count as zero
+constexpr double kFloor = -1000.0;    // exponents below count as zero, and so do sums of a chunk below 2^-900:
+constexpr double kNothing = 0x1p-900;  // there they are taken for 2^-1000
 constexpr double kUnset = -1.0e300;   // reference of a part without an unmasked entry
 
 // What is needed of a row, or a part of one: sum of 2^(c (s - ref)), NaN if a score is NaN or +inf.  The reference is the
@@ -363,13 +364,10 @@ __device__ __forceinline__ bool drawable(const Draw& d) {
     return d.row >= 0 && d.log_p > -(double)INFINITY && (!d.with_q || d.rho == d.rho);  // (NaN: no)
 }
 
-// An entry's exponentials: p's, 0 in the column that is left out, and q's.
-struct Pair {
-    double e, h;
-};
-__device__ __forceinline__ Pair pair_of(const VfArgs& A, const Draw& d, float s, float t, int64_t j) {
-    const double e = pow2_or_zero(((double)s - d.ref_p) * A.c);
-    return {j == d.out ? 0.0 : e, d.with_q ? pow2_or_zero(((double)t - d.ref_q) * A.cq) : 0.0};
+// The exponential of a score over its row's largest: 0 below the floor; or, where that is told apart later, 2^-1000.
+__device__ __forceinline__ double exp_of(float s, double ref, double c) { return pow2_or_zero(((double)s - ref) * c); }
+__device__ __forceinline__ double exp_near(float s, double ref, double c, double floor) {
+    return pow2(fmax((double)s - ref, floor), c);
 }
 
 // Sums over a chunk, by a wave: of e, of h, of max(e - rho h, 0) and of h where that is positive (without q: of e).
@@ -380,36 +378,45 @@ __device__ __forceinline__ void chunk_sums(const VfArgs& A, const Draw& d, int c
     const int start = chunk * A.chunk_len, j0 = start + lane * VE, size = min(A.chunk_len, A.m - start);
     const E* s = static_cast<const E*>(A.s) + d.row * A.ld + j0;
     const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld) + j0;
+    const double floor = kFloor / A.c, floor_q = kFloor / A.cq;
     double e = 0.0, h = 0.0, rest = 0.0, hot = 0.0;
-    auto add = [&](float x, float y, int j) {
-        const Pair p = pair_of(A, d, x, y, j);
-        const double w = fma(-d.rho, p.h, p.e);
-        e += p.e;
-        if (d.with_q) {
-            h += p.h;
-            rest += fmax(w, 0.0);
-            hot += w > 0.0 ? p.h : 0.0;
-        }
+    auto add_both = [&](float x, float y) {
+        const double a = exp_near(x, d.ref_p, A.c, floor), b = exp_near(y, d.ref_q, A.cq, floor_q), w = fma(-d.rho, b, a);
+        e += a;
+        h += b;
+        rest += fmax(w, 0.0);
+        hot += w > 0.0 ? b : 0.0;
     };
-    if (size == A.chunk_len) {
+    auto add_one = [&](float x, int j) { e += j == d.out ? 0.0 : exp_near(x, d.ref_p, A.c, floor); };
+    const int whole = size / (64 * VE) * (64 * VE);  // entries in whole runs of all lanes
+    // (the loops are not unrolled: a wave has few chunks, and cold code takes longer to fetch than to run)
+    if (d.with_q) {
         Run16<T> a, b, a1, b1;
-        a1.get(s);
-        b1.get(q);
+        if (whole > 0) a1.get(s), b1.get(q);
 #pragma unroll 1
-        for (int at = 0; at < size; at += 64 * VE) {
+        for (int at = 0; at < whole; at += 64 * VE) {
             a = a1;
             b = b1;
-            const int next = at + 64 * VE < size ? at + 64 * VE : at;
+            const int next = at + 64 * VE < whole ? at + 64 * VE : at;
             a1.get(s + next);
             b1.get(q + next);
 #pragma unroll
-            for (int c = 0; c < VE; ++c) add(a.at(c), b.at(c), j0 + at + c);
+            for (int c = 0; c < VE; ++c) add_both(a.at(c), b.at(c));
         }
+#pragma unroll 1
+        for (int j = whole + lane; j < size; j += 64) add_both(T::to(s[j - lane * VE]), T::to(q[j - lane * VE]));
     } else {
+        Run16<T> a, a1;
+        if (whole > 0) a1.get(s);
 #pragma unroll 1
-        for (int at = 0; at < size; at += 64 * VE)
+        for (int at = 0; at < whole; at += 64 * VE) {
+            a = a1;
+            a1.get(s + (at + 64 * VE < whole ? at + 64 * VE : at));
+#pragma unroll
+            for (int c = 0; c < VE; ++c) add_one(a.at(c), j0 + at + c);
+        }
 #pragma unroll 1
-            for (int c = 0; c < VE && at + lane * VE + c < size; ++c) add(T::to(s[at + c]), T::to(q[at + c]), j0 + at + c);
+        for (int j = whole + lane; j < size; j += 64) add_one(T::to(s[j - lane * VE]), start + j);
     }
     if (!d.with_q) {
         e = lanes_sum<64>(e);
@@ -494,7 +501,8 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
     }
     auto weight_of = [&](int k) {
         if (k >= A.chunks) return 0.0;
-        return d.with_q ? fmax(fma(shift, sums[4 * k + 3], sums[4 * k + 2]), 0.0) : sums[4 * k];
+        const double w = d.with_q ? fma(shift, sums[4 * k + 3], sums[4 * k + 2]) : sums[4 * k];
+        return w > kNothing ? w : 0.0;
     };
     double mine = 0.0, upto = 0.0, here, total = 0.0;
     for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
@@ -538,7 +546,7 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
     const double prior = L.prior;
     // inside it, each thread some neighbouring entries
     const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
-    const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
+    const E* t = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);
     const int j0 = at * A.chunk_len + tid * kPer, end = min(A.m, (at + 1) * A.chunk_len);
     double w[kPer];
     mine = 0.0;
@@ -548,18 +556,19 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
         E a[kPer], b[kPer];
         if (j0 + kPer <= end) {
             __builtin_memcpy(a, s + j0, sizeof(a));
-            __builtin_memcpy(b, q + j0, sizeof(b));
+            __builtin_memcpy(b, t + j0, sizeof(b));
         } else {
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 a[e] = s[min(j0 + e, end - 1)];
-                b[e] = q[min(j0 + e, end - 1)];
+                b[e] = t[min(j0 + e, end - 1)];
             }
         }
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const Pair p = pair_of(A, d, T::to(a[e]), T::to(b[e]), j0 + e);
-            w[e] = j0 + e < end ? fmax(fma(-d.rho, p.h, p.e), 0.0) : 0.0;
+            const double p = j0 + e == d.out ? 0.0 : exp_of(T::to(a[e]), d.ref_p, A.c);
+            const double q = d.with_q ? exp_of(T::to(b[e]), d.ref_q, A.cq) : 0.0;
+            w[e] = j0 + e < end ? fmax(fma(-d.rho, q, p), 0.0) : 0.0;
             mine += w[e];
         }
     }
@@ -586,7 +595,7 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
 // Where each request stops and the sums of the chunks of what it draws from: a wave per chunk, A.parts workgroups per
 // request; one that has all the chunks draws too.
 template <class T>
-__global__ __launch_bounds__(kBlock) void k_verify_chunks(VfArgs A) {
+__global__ __launch_bounds__(kBlock, 4) void k_verify_chunks(VfArgs A) {
     __shared__ Look L;
     __shared__ Pick P;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
