@@ -244,28 +244,6 @@ struct Run16 {
     // Holds the run as it was loaded up to here: its conversions to float32, twice the registers, stay behind.
     __device__ __forceinline__ void held() { asm("" : "+v"(raw.x), "+v"(raw.y), "+v"(raw.z), "+v"(raw.w)); }
     __device__ __forceinline__ void put(Elem* p) const { __builtin_memcpy(p, &raw, 16); }
-    // Run q of a row of d elements: behind the row's end the elements read as 0 and are not written.
-    __device__ __forceinline__ void load(const Elem* row, int64_t q, int64_t d) {
-        const int64_t j = q * n;
-        if (j + n <= d) {
-            get(row + j);
-        } else {
-            Elem v[n];
-#pragma unroll
-            for (int i = 0; i < n; ++i) v[i] = j + i < d ? row[j + i] : Elem(0);
-            set(v);
-        }
-    }
-    __device__ __forceinline__ void store(Elem* row, int64_t q, int64_t d) const {
-        const int64_t j = q * n;
-        if (j + n <= d) {
-            put(row + j);
-        } else {
-#pragma unroll
-            for (int i = 0; i < n - 1; ++i)
-                if (j + i < d) row[j + i] = bits(i);
-        }
-    }
 };
 
 // LDS written by this wave's lanes is visible to its other lanes (one wave's
