@@ -25,6 +25,7 @@ A trainer wraps a forward and its gradient in a ``torch.autograd.Function``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -583,7 +584,7 @@ def _scores(scores, name: str = "scores", shape: str = "(n, m)"):
         raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {scores.dtype})")
     if scores.dim() != 2:
         raise ValueError(f"{name} must be {shape} (got shape {tuple(scores.shape)})")
-    if scores.device.type != "cuda":
+    if not scores.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
     n, m = scores.shape
     ld = scores.stride(0)
@@ -605,10 +606,18 @@ def _grad_buf(grad, scores):
     return grad
 
 
+def _is(t, shape, dtype, device) -> bool:
+    """Whether t is a contiguous tensor of this shape, type and device (a call on a few rows is bound by the host)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device)
+
+
 def _vec(t, n, dtype, device, name):
     """An optional (n,) input (or of shape n, a tuple), contiguous."""
     if t is None:
         return None
+    if _is(t, n if isinstance(n, tuple) else (n,), dtype, device):
+        return t
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor on {device}")
     if tuple(t.shape) != (n if isinstance(n, tuple) else (n,)):
@@ -622,7 +631,9 @@ def _addr(t: torch.Tensor | None):
 
 def _out(t, shape, dtype, device, name: str) -> torch.Tensor:
     """_buf, without its checks where there is nothing to check (a call on a few rows is bound by the host)."""
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else _buf(t, shape, dtype, device, name)
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return t if _is(t, shape, dtype, device) else _buf(t, shape, dtype, device, name)
 
 
 def _call(name: str, device, *args):
@@ -630,7 +641,7 @@ def _call(name: str, device, *args):
     fn = getattr(_lib or load_library(), name)
     # the handle alone: a Stream object for it costs as much host time as a third of a small call
     stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         code = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -811,12 +822,17 @@ class Verified(NamedTuple):
     logp: torch.Tensor
 
 
-def scores_verify_workspace(dtype: torch.dtype, n: int, m: int, b: int, device) -> torch.Tensor:
-    """A workspace tensor for scores_verify of b requests on an (n, m) score matrix of this dtype."""
+@functools.lru_cache(maxsize=256)
+def _verify_bytes(dtype, n, m, b):
     nb = int(load_library().sk_scores_verify_workspace_bytes(DTYPES.get(dtype, -1), n, m, b))
     if nb == 0:
         raise ValueError(f"invalid arguments for scores_verify (dtype={dtype} n={n} m={m} b={b}: m <= 2**30)")
-    return torch.empty(nb, dtype=torch.uint8, device=device)
+    return nb
+
+
+def scores_verify_workspace(dtype: torch.dtype, n: int, m: int, b: int, device) -> torch.Tensor:
+    """A workspace tensor for scores_verify of b requests on an (n, m) score matrix of this dtype."""
+    return torch.empty(_verify_bytes(dtype, n, m, b), dtype=torch.uint8, device=device)
 
 
 def scores_verify(scores, tokens: torch.Tensor, starts: torch.Tensor, u_accept: torch.Tensor | None,
@@ -848,7 +864,7 @@ def scores_verify(scores, tokens: torch.Tensor, starts: torch.Tensor, u_accept: 
         draft, code_q, nq, mq, ld_q = _scores(draft, "draft")
         if code_q != code or (nq, mq) != (n, m) or draft.device != dev:
             raise ValueError(f"draft must be a {s.dtype} tensor of shape {(n, m)} on {dev}")
-    ws = _ws(ws, dev, lambda: scores_verify_workspace(s.dtype, n, m, b, dev))
+    ws = scores_verify_workspace(s.dtype, n, m, b, dev) if ws is None else _ws(ws, dev, None)
     o_acc, o_next, o_tok, o_ratio, o_logp = out or (None,) * 5
     acc = _out(o_acc, (b,), torch.int32, dev, "out.accepted")
     nxt = _out(o_next, (b,), torch.int64, dev, "out.next")
@@ -872,6 +888,7 @@ class RoutePlan(NamedTuple):
     align: int = 1
 
 
+@functools.lru_cache(maxsize=256)
 def route_sort_rows(n: int, k: int, m: int, align: int = 1, capacity: int = 0) -> int:
     """Rows that the sorted choices of n tokens can take at most (the length of a plan's source)."""
     rows = int(load_library().sk_route_sort_rows(n, k, m, align, capacity))
@@ -881,12 +898,17 @@ def route_sort_rows(n: int, k: int, m: int, align: int = 1, capacity: int = 0) -
     return rows
 
 
-def route_sort_workspace(n: int, k: int, m: int, device) -> torch.Tensor:
-    """A workspace tensor for route_sort of (n, k) choices among m experts."""
+@functools.lru_cache(maxsize=256)
+def _sort_bytes(n, k, m):
     nb = int(load_library().sk_route_sort_workspace_bytes(n, k, m))
     if nb == 0:
         raise ValueError(f"invalid problem size n={n} k={k} m={m} (1 <= k <= 64, 1 <= m <= 1024, n * k < 2**31)")
-    return torch.empty(nb, dtype=torch.uint8, device=device)
+    return nb
+
+
+def route_sort_workspace(n: int, k: int, m: int, device) -> torch.Tensor:
+    """A workspace tensor for route_sort of (n, k) choices among m experts."""
+    return torch.empty(_sort_bytes(n, k, m), dtype=torch.uint8, device=device)
 
 
 def route_sort(idx: torch.Tensor, m: int, *, align: int = 1, capacity: int = 0, ws: torch.Tensor | None = None,
@@ -901,13 +923,13 @@ def route_sort(idx: torch.Tensor, m: int, *, align: int = 1, capacity: int = 0, 
     if idx.dtype != torch.int32 or idx.dim() != 2:
         raise ValueError(f"idx must be an (n, k) int32 tensor (got {idx.dtype} of shape {tuple(idx.shape)})")
     dev = idx.device
-    if dev.type != "cuda":
+    if not idx.is_cuda:
         raise ValueError("idx must be on a GPU device")
     n, k = idx.shape
     m, align, capacity = int(m), int(align), int(capacity)
     rows = route_sort_rows(n, k, m, align, capacity)
     idx = idx.contiguous()
-    ws = _ws(ws, dev, lambda: route_sort_workspace(n, k, m, dev))
+    ws = route_sort_workspace(n, k, m, dev) if ws is None else _ws(ws, dev, None)
     o_slot, o_source, o_counts, o_offsets, _ = out or (None,) * 5
     slot = _out(o_slot, (n, k), torch.int32, dev, "out.slot")
     source = torch.empty(rows, dtype=torch.int32, device=dev) if o_source is None else _at_least(
