@@ -15,7 +15,9 @@ Potentials are returned in cost units (f, g), not divided by eps.
 
 The scores_* functions take a score matrix instead of clouds, (n, m) float32,
 bfloat16 or float16 with any row stride: balancing potentials and routing of a
-router's scores, log-probabilities of a head's, and their gradients.
+router's scores, log-probabilities of a head's, and their gradients, and the
+verification of drafted tokens.  The route_* functions carry token rows, (n, d) of
+the same types, to the experts that a routing chose and back.
 
 No function here takes part in autograd: inputs are read and outputs written by
 their addresses, so a result carries no graph, also where an input requires a

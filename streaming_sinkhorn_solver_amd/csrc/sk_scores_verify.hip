@@ -16,8 +16,10 @@
 // exponentials of p's and q's row and rho the quotient of their sums, the residual is
 // max(e - rho h, 0).  One pass takes sum e and sum h, which give rho, and with rho0 from the
 // float32 sums R = sum max(e - rho0 h, 0) and B = sum of h where e > rho0 h.  The residual's
-// sum is then R + (rho0 - rho) B but for entries between the two quotients, which are off by
-// their distance 2^-20 and a share of 2^-20 of all.
+// sum is then R + (rho0 - rho) B but for entries whose e / h lies between the two quotients,
+// some 2^-22 apart: each is off by that share of itself, and in general they are that share of
+// all.  (Were p and q proportional over much of the row, their sums alike to 2^-22 and yet
+// not equal, a draw would be exact to that distance of a border only.)
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -28,11 +30,12 @@ namespace {
 constexpr int64_t kVfGrid = 1 << 20;  // workgroups of one launch (each may serve several rows)
 constexpr int64_t kVfMaxCols = (int64_t)1 << 30;
 constexpr int kVfVecs = 4;             // 16-byte loads of a thread's block
-constexpr int kVfChunkMost = 2048;    // entries of the residual whose sum is kept: 512, 1024 or 2048
-constexpr int kVfFill = 1024, kVfCutMin = 1024;
-constexpr double kFloor = -1000.0;    // exponents below count as zero, and so do sums of a chunk below 2^-900:
-constexpr double kNothing = 0x1p-900;  // there they are taken for 2^-1000
-constexpr double kUnset = -1.0e300;   // reference of a part without an unmasked entry
+constexpr int kVfChunkMost = 2048;     // entries of a chunk: 512, 1024 or this
+constexpr int kVfFill = 1024;          // workgroups that a launch is cut into where it has fewer,
+constexpr int kVfCutMin = 1024;        // no part of a row below so many 16-byte loads
+constexpr double kFloor = -1000.0;     // exponents below count as zero; in the chunks' sums they count as 2^-1000,
+constexpr double kNothing = 0x1p-900;  // and sums below this as zero
+constexpr double kUnset = -1.0e300;    // reference of what is no part of a row
 
 // What is needed of a row, or a part of one: sum of 2^(c (s - ref)), NaN if a score is NaN or +inf.  The reference is the
 // largest score, and the difference to it is taken first: rows of a type's lowest value lose nothing.
