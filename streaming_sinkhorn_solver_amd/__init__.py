@@ -931,15 +931,25 @@ def route_sort(idx: torch.Tensor, m: int, *, align: int = 1, capacity: int = 0, 
     m, align, capacity = int(m), int(align), int(capacity)
     rows = route_sort_rows(n, k, m, align, capacity)
     idx = idx.contiguous()
-    ws = route_sort_workspace(n, k, m, dev) if ws is None else _ws(ws, dev, None)
-    o_slot, o_source, o_counts, o_offsets, _ = out or (None,) * 5
-    slot = _out(o_slot, (n, k), torch.int32, dev, "out.slot")
-    source = torch.empty(rows, dtype=torch.int32, device=dev) if o_source is None else _at_least(
-        o_source, rows, torch.int32, dev, "out.source")
-    counts = _out(o_counts, (m,), torch.int32, dev, "out.counts")
-    offsets = _out(o_offsets, (m + 1,), torch.int32, dev, "out.offsets")
+    if out is None:
+        # one allocation for all (a call on a few tokens is bound by the host); the workspace, first, is aligned by it
+        own = 0 if ws is not None else _sort_bytes(n, k, m) // 4
+        buf = torch.empty(own + n * k + rows + 2 * m + 1, dtype=torch.int32, device=dev)
+        own_ws, slot, source, counts, offsets = buf.split_with_sizes((own, n * k, rows, m, m + 1))
+        slot = slot.view(n, k)
+        ws_ptr, ws_bytes = own_ws.data_ptr(), 4 * own
+    else:
+        slot = _out(out.slot, (n, k), torch.int32, dev, "out.slot")
+        source = _at_least(out.source, rows, torch.int32, dev, "out.source")
+        counts = _out(out.counts, (m,), torch.int32, dev, "out.counts")
+        offsets = _out(out.offsets, (m + 1,), torch.int32, dev, "out.offsets")
+        if ws is None:
+            ws = route_sort_workspace(n, k, m, dev)
+    if ws is not None:
+        ws = _ws(ws, dev, None)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     _call("sk_route_sort", dev, idx.data_ptr(), n, k, m, align, capacity, slot.data_ptr(), source.data_ptr(),
-          source.numel(), counts.data_ptr(), offsets.data_ptr(), ws.data_ptr(), ws.numel())
+          source.numel(), counts.data_ptr(), offsets.data_ptr(), ws_ptr, ws_bytes)
     return RoutePlan(slot, source, counts, offsets, align)
 
 
