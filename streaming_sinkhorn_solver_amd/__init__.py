@@ -866,16 +866,27 @@ def scores_verify(scores, tokens: torch.Tensor, starts: torch.Tensor, u_accept: 
         draft, code_q, nq, mq, ld_q = _scores(draft, "draft")
         if code_q != code or (nq, mq) != (n, m) or draft.device != dev:
             raise ValueError(f"draft must be a {s.dtype} tensor of shape {(n, m)} on {dev}")
-    ws = scores_verify_workspace(s.dtype, n, m, b, dev) if ws is None else _ws(ws, dev, None)
-    o_acc, o_next, o_tok, o_ratio, o_logp = out or (None,) * 5
-    acc = _out(o_acc, (b,), torch.int32, dev, "out.accepted")
-    nxt = _out(o_next, (b,), torch.int64, dev, "out.next")
-    tok = _out(o_tok, (n,), torch.int64, dev, "out.tokens")
-    ratio = _out(o_ratio, (n,), torch.float32, dev, "out.ratio")
-    logp = _out(o_logp, (n,), torch.float32, dev, "out.logp")
+    if out is None:
+        # two allocations for all (a call on a few rows is bound by the host); the workspace, first, is aligned by it
+        own = 0 if ws is not None else _verify_bytes(s.dtype, n, m, b) // 4
+        own_ws, ratio, logp, acc = torch.empty(own + 2 * n + b, dtype=torch.float32, device=dev).split_with_sizes((own, n, n, b))
+        acc = acc.view(torch.int32)
+        tok, nxt = torch.empty(n + b, dtype=torch.int64, device=dev).split_with_sizes((n, b))
+        ws_ptr, ws_bytes = own_ws.data_ptr(), 4 * own
+    else:
+        acc = _out(out.accepted, (b,), torch.int32, dev, "out.accepted")
+        nxt = _out(out.next, (b,), torch.int64, dev, "out.next")
+        tok = _out(out.tokens, (n,), torch.int64, dev, "out.tokens")
+        ratio = _out(out.ratio, (n,), torch.float32, dev, "out.ratio")
+        logp = _out(out.logp, (n,), torch.float32, dev, "out.logp")
+        if ws is None:
+            ws = scores_verify_workspace(s.dtype, n, m, b, dev)
+    if ws is not None:
+        ws = _ws(ws, dev, None)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     _call("sk_scores_verify", dev, s.data_ptr(), code, n, m, ld, float(eps), _addr(draft), ld_q, float(eps_draft),
           tokens.data_ptr(), starts.data_ptr(), b, _addr(u_accept), _addr(u_sample), acc.data_ptr(), nxt.data_ptr(),
-          tok.data_ptr(), ratio.data_ptr(), logp.data_ptr(), ws.data_ptr(), ws.numel())
+          tok.data_ptr(), ratio.data_ptr(), logp.data_ptr(), ws_ptr, ws_bytes)
     return Verified(acc, nxt, tok, ratio, logp)
 
 
