@@ -115,6 +115,7 @@ __device__ __forceinline__ Sum join(Sum a, Sum b, double c) {
     const double ref = fmax(a.ref, b.ref);
     return {ref, moved(a, ref, c) + moved(b, ref, c)};
 }
+
 // Whether row i of the target (of the draft) is one that a request looks at.  All lanes of a wave, i the same in each.
 __device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draft, int lane) {
     const int64_t lowest = A.starts[0], end = A.starts[A.b], here = A.tokens[i], before = A.tokens[i > 0 ? i - 1 : 0];
@@ -127,9 +128,9 @@ __device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draf
         const uint64_t mask = __ballot(at < lo + size && A.starts[min(at, A.b)] <= i);
         const int below = __popcll(mask);
         if (below == 0) return false;
-        const int64_t end = lo + size;
+        const int64_t rest = size - (int64_t)(below - 1) * step;
         lo += (int64_t)(below - 1) * step;
-        size = min(step, end - lo);
+        size = min(step, rest);
     }
     return __ballot(lane < size && A.starts[min(lo + lane, A.b)] == i) != 0;
 }
@@ -530,7 +531,8 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
         }
         return;
     }
-    // the first chunk whose sum with those before exceeds the mark; where roundings leave none, the last with a sum
+    // the first chunk whose sum with those before exceeds the mark; where none does (u_sample = 1), the last whose sum is
+    // more than roundings
     const double mark = (double)fminf(fmaxf(A.u_sample[r], 0.0f), 1.0f) * total;
     int at = -1;
     double before = 0.0;
@@ -541,12 +543,13 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
             upto = before + block_scan(mine, L.scan, here);
             before += here;
         }
-        const int hit = first_over(mine > 0.0 && upto > mark, mine > 0.0, L, found);
+        const int hit = first_over(mine > 0.0 && upto > mark, mine > 0x1p-44 * all, L, found);
         if (hit >= 0) at = k0 + hit;
         if (tid == hit) L.prior = upto - mine;
     }
     __syncthreads();
-    const double prior = L.prior;
+    const double prior = at < 0 ? total : L.prior;
+    if (at < 0) at = A.chunks - 1;
     // inside it, each thread some neighbouring entries
     const E* s = static_cast<const E*>(A.s) + d.row * A.ld;
     const E* t = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld);

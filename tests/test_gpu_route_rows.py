@@ -72,9 +72,10 @@ def test_sort_one_expert_or_none(n, k, m):
             assert np.array_equal(got.cpu().numpy(), ref)
 
 
-def test_sort_many_choices():
-    """More workgroups than add up one another's counts (1048576 choices)."""
-    n, k, m = 140001, 8, 300
+@pytest.mark.parametrize("m", [300, 1000])
+def test_sort_many_choices(m):
+    """69 workgroups: more than add up one another's counts among 1000 experts, not among 300."""
+    n, k = 140001, 8
     idx = choices(n, k, m, 4, 0.1)
     plan = sk.route_sort(gpu(idx), m, align=16)
     flat = idx.reshape(-1).astype(np.int64)
