@@ -21,7 +21,8 @@ constexpr int kRowsMaxTop = 64;
 // equal expert find one another by one ballot per bit of its number, so a pair's rank
 // among the wave's pairs of its expert is a count of lower lanes beside the wave's own
 // counter in LDS.  Adding the counts of the waves and workgroups before gives the rank
-// among all.
+// among all.  131072 choices among 256 take 10.5 us: two launches, the second (7.5) bound
+// by its instructions, 560 in each of a workgroup's 16 waves.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortMost = 16;      // pairs per thread at most: a wave's counter fits 16 bits
 constexpr int kSortOne = 4096;     // pairs that one workgroup takes alone
@@ -202,11 +203,11 @@ hipError_t launch_place(const SortArgs& A, hipStream_t s) {
 // How the pairs are shared out: per workgroup a power-of-two number of pairs per thread.
 struct SortPlan {
     int per_thread, groups;
-    size_t hist, total;
+    size_t total;
 };
 
 SortPlan sort_plan(int64_t pairs, int64_t m) {
-    SortPlan P{1, 1, 0, 256};
+    SortPlan P{1, 1, 256};
     const int64_t most = pairs <= kSortOne ? 1 : sort_groups(m);
     while (P.per_thread < kSortMost && (int64_t)P.per_thread * kSortThreads * most < pairs) P.per_thread *= 2;
     const int64_t per = (int64_t)P.per_thread * kSortThreads;
@@ -238,7 +239,8 @@ struct RowsArgs {
     int lanes;         // of a token: a power of two up to the workgroup
     int whole, pieces, rest;  // whole pieces of a row, all of them, and the elements behind the whole ones
     bool apart;        // the output is no input
-    int64_t token_groups;  // groups of kBlock / lanes tokens
+    int parts, span;       // workgroups that share a token's row, and the pieces of each
+    int64_t token_groups;  // groups of kBlock / lanes tokens, times parts
     int64_t grid;          // workgroups that take them in turn
     int pad_parts;         // workgroups behind them for each expert's padding, 0: there is none
     const int32_t *slot, *counts, *offsets;
@@ -271,15 +273,22 @@ __device__ void clear_padding(const RowsArgs& A) {
     }
 }
 
-// f(token, lane in the token's group) for the thread's tokens.  ONE: all lanes of a wave have the same token.
+// f(token, lane in the token's group, first and last piece) for the thread's tokens.  ONE: all lanes of a wave have the
+// same token.
 template <bool ONE, class F>
 __device__ __forceinline__ void each_token(const RowsArgs& A, F f) {
     int in_group = threadIdx.x / A.lanes;
     const int lane = threadIdx.x % A.lanes;
     if (ONE) in_group = __builtin_amdgcn_readfirstlane(in_group);
     for (int64_t g = blockIdx.x; g < A.token_groups; g += A.grid) {
-        const int64_t i = g * (kBlock / A.lanes) + in_group;
-        if (i < A.n) f(i, lane);
+        int64_t i = g * (kBlock / A.lanes) + in_group;
+        int q0 = 0, q1 = A.pieces;
+        if (ONE && A.parts > 1) {
+            i = (uint32_t)g / (uint32_t)A.parts;
+            q0 = (int)(g - i * A.parts) * A.span;
+            q1 = min(A.pieces, q0 + A.span);
+        }
+        if (i < A.n) f(i, lane, q0 + lane, q1);
     }
 }
 
@@ -291,7 +300,7 @@ __global__ __launch_bounds__(kBlock) void k_dispatch(RowsArgs A) {
     using E = typename T::type;
     constexpr int VE = Run16<T>::n;
     if (blockIdx.x >= A.grid) return clear_padding<T>(A);
-    each_token<ONE>(A, [&](int64_t i, int lane) {
+    each_token<ONE>(A, [&](int64_t i, int lane, int q0, int q1) {
         const E* x = static_cast<const E*>(A.tokens) + i * A.ld_tokens;
         const int32_t* slot = A.slot + i * A.k;
         const float* weights = A.weights ? A.weights + i * A.k : nullptr;
@@ -301,7 +310,7 @@ __global__ __launch_bounds__(kBlock) void k_dispatch(RowsArgs A) {
                 if (in_rows(A, s)) f(static_cast<E*>(A.out) + s * A.ld_out, weights ? weights[r] : 1.0f);
             }
         };
-        for (int q = lane; q < A.pieces; q += A.lanes) {
+        for (int q = q0; q < q1; q += A.lanes) {
             const int j = piece_at<T>(A, q);
             Run16<T> v;
             v.get(x + j);
@@ -335,12 +344,12 @@ template <class T, bool ONE, bool REST>
 __global__ __launch_bounds__(kBlock) void k_combine(RowsArgs A) {
     using E = typename T::type;
     constexpr int VE = Run16<T>::n;
-    each_token<ONE>(A, [&](int64_t i, int lane) {
+    each_token<ONE>(A, [&](int64_t i, int lane, int q0, int q1) {
         const int32_t* slot = A.slot + i * A.k;
         const float* weights = A.weights ? A.weights + i * A.k : nullptr;
         const E* add = A.add ? static_cast<const E*>(A.add) + i * A.ld_add : nullptr;
         E* out = static_cast<E*>(A.out) + i * A.ld_out;
-        for (int q = lane; q < A.pieces; q += A.lanes) {
+        for (int q = q0; q < q1; q += A.lanes) {
             const int j = REST ? piece_at<T>(A, q) : q * VE;
             float y[VE];
             Run16<T> v[kAhead];
@@ -493,13 +502,25 @@ void share(RowsArgs& A, int least) {
     A.pieces = A.whole + (A.whole > 0 && A.rest > 0 ? 1 : 0);
     A.lanes = least;
     while (A.lanes < kBlock && A.lanes < (A.whole > 0 ? A.pieces : A.d)) A.lanes *= 2;
+    A.parts = 1;
+    A.span = A.pieces;
     A.pad_parts = A.counts ? std::min(16, std::max(1, 1024 / A.m)) : 0;
+}
+
+// Few tokens with long rows: several workgroups for each, every one with a run of pieces (1 x 8 rows of 8192 bf16: the sum
+// takes 4.7 us so, 10.5 in one workgroup).
+void split_rows(RowsArgs& A) {
+    const int most = (A.pieces + kBlock - 1) / kBlock;
+    if (A.lanes < kBlock || A.n > 512 || most < 2) return;
+    const int each = (most + std::min(most, (int)(1024 / A.n)) - 1) / std::min(most, (int)(1024 / A.n));
+    A.span = each * kBlock;
+    A.parts = (A.pieces + A.span - 1) / A.span;
 }
 
 template <class K>
 hipError_t launch_rows(RowsArgs A, K kernel, hipStream_t s) {
     const int per = kBlock / A.lanes;
-    A.token_groups = (A.n + per - 1) / per;
+    A.token_groups = (A.n + per - 1) / per * A.parts;
     A.grid = std::min(A.token_groups, kRowsGrid);
     hipLaunchKernelGGL(kernel, dim3((unsigned)(A.grid + (int64_t)A.pad_parts * A.m)), dim3(kBlock), 0, s, A);
     return hipGetLastError();
@@ -508,6 +529,7 @@ hipError_t launch_rows(RowsArgs A, K kernel, hipStream_t s) {
 template <class T>
 hipError_t dispatch(RowsArgs A, hipStream_t s) {
     share<T>(A, 4);
+    split_rows(A);
     const bool lines = reinterpret_cast<uintptr_t>(A.out) % 128 == 0 && A.ld_out * (int64_t)sizeof(typename T::type) % 128 == 0;
     auto kernel = A.lanes < 64 ? k_dispatch<T, false, false> : lines ? k_dispatch<T, true, true> : k_dispatch<T, true, false>;
     return launch_rows(A, kernel, s);
@@ -516,6 +538,7 @@ hipError_t dispatch(RowsArgs A, hipStream_t s) {
 template <class T>
 hipError_t combine(RowsArgs A, hipStream_t s) {
     share<T>(A, 4);
+    split_rows(A);
     A.apart = A.add != A.out;
     auto kernel = A.rest ? (A.lanes >= 64 ? k_combine<T, true, true> : k_combine<T, false, true>)
                          : (A.lanes >= 64 ? k_combine<T, true, false> : k_combine<T, false, false>);

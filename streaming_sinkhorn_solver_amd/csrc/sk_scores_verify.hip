@@ -139,7 +139,8 @@ __device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draf
 __device__ __forceinline__ float rescaled(float S, float M, float top, float c) { return S * s_ex2((M - top) * c); }
 
 // Sums of the rows' exponentials in float32: a row, or a part of one, per W waves, each thread with a running maximum
-// that it moves once per kVfVecs loads.  (A NaN or +inf score makes the sum NaN by itself.)
+// that it moves once per kVfVecs loads.  (A NaN or +inf score makes the sum NaN by itself.)  Bound by memory: 512 rows
+// of 131072 bf16 take 26 us, 5.2 TB/s; in float64 they took 59, bound by 17 instructions per score of 5 to 6 cycles each.
 template <class T, int W>
 __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
     using E = typename T::type;
@@ -599,7 +600,8 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
 }
 
 // Where each request stops and the sums of the chunks of what it draws from: a wave per chunk, A.parts workgroups per
-// request; one that has all the chunks draws too.
+// request; one that has all the chunks draws too.  Bound by the issue of some 40 float64 instructions per entry: 64
+// requests over 131072 columns take 22 us, 5 of them to look where each stops.
 template <class T>
 __global__ __launch_bounds__(kBlock, 4) void k_verify_chunks(VfArgs A) {
     __shared__ Look L;
@@ -622,6 +624,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_verify_chunks(VfArgs A) {
     }
 }
 
+// Bound by the latency of its loads and of three sums over the workgroup: 6 us for one request, 8 for 64.
 template <class T>
 __global__ __launch_bounds__(kBlock) void k_verify_draw(VfArgs A) {
     __shared__ Pick P;
@@ -636,6 +639,7 @@ __global__ __launch_bounds__(kBlock) void k_verify_draw(VfArgs A) {
 
 // ----- greedy: p is one at the row's largest score, the first of equal ones -----------------
 // Part: (ordered score, ~column) of the largest entry; 0: no unmasked entry; all ones: a NaN or +inf score.
+// Bound by memory: 320 rows of 65536 f16 take 8 us, 5.2 TB/s.
 template <class T, int W>
 __global__ __launch_bounds__(kBlock) void k_verify_best(VfArgs A) {
     using E = typename T::type;

@@ -168,6 +168,27 @@ def test_rows(d, dtype):
         close(d_w, want_w, (d / 16 + 20) * U * size, "d_weights")
 
 
+@pytest.mark.parametrize("n,d", [(1, 8195), (3, 16384), (129, 4100), (512, 4096), (513, 4096), (600, 4099)])
+def test_long_rows(n, d):
+    """Rows that a workgroup does not take at once: shared out among several (up to 512 tokens), or taken in turns."""
+    k, m = 2, 3
+    idx = choices(n, k, m, n)
+    plan = sk.route_sort(gpu(idx), m, align=2)
+    slot, _, _, offsets = oro.sort(idx, m, 2)
+    rows = plan.source.numel()
+    w = np.random.default_rng(n).normal(size=(n, k)).astype(np.float32)
+    x, xs = random_window(n, d, "bf16", 1, 1, 1)
+    g, gs = random_window(rows, d, "bf16", 2)
+    out = sk.route_dispatch(x, plan, gpu(w), out=torch.full((rows, d), 7.0, dtype=torch.bfloat16, device=DEV))
+    want = oro.dispatch(xs, slot, offsets, w, np.full((rows, d), 7.0))
+    close(out, want, product_tol(want, "bf16"), "dispatch")
+    want = oro.combine(gs, slot, w, xs)
+    close(sk.route_combine(g, plan, gpu(w), add=x), want, sum_tol(want, oro.combine(np.abs(gs), slot, np.abs(w), np.abs(xs)), k + 1, "bf16"), "combine")
+    over = x.clone(memory_format=torch.contiguous_format)
+    sk.route_combine(g, plan, gpu(w), add=over, out=over)
+    assert torch.equal(over, sk.route_combine(g, plan, gpu(w), add=x))
+
+
 @pytest.mark.parametrize("k", [1, 2, 7, 8, 9, 16, 17, 64])
 @pytest.mark.parametrize("d", [8, 200, 2048])
 def test_many_choices_of_a_token(k, d):
