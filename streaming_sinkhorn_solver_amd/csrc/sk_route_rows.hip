@@ -9,6 +9,7 @@
 #include "sk_scores.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sk {
 namespace {
@@ -322,10 +323,7 @@ __global__ __launch_bounds__(kBlock) void k_dispatch(RowsArgs A) {
                     for (int c = 0; c < VE; ++c) f[c] = w * v.at(c);
                     o.round(f);
                 }
-                if constexpr (ONCE)
-                    o.put_once(row + j);
-                else
-                    o.put(row + j);
+                o.template store<ONCE>(row + j);
             });
         }
         if (A.pieces == 0 && lane < A.d) {
@@ -335,15 +333,15 @@ __global__ __launch_bounds__(kBlock) void k_dispatch(RowsArgs A) {
     });
 }
 
-constexpr int kAhead = 8;  // rows of a token whose pieces are in flight
+constexpr int kAheadMost = 8;  // rows of a token whose pieces are in flight
 
 // y = add + sum_r w_r rows[slot_r], in the order of r, float32, rounded once.  Bound by the rows' reads: 16384 x 8 rows
-// of 2048 f16 take 105 us, 6.4 TB/s.  They and y pass the caches by (131 us otherwise).
-// REST: rows that do not end with a whole piece.
-template <class T, bool ONE, bool REST>
+// of 2048 f16 take 105 us, 6.4 TB/s.
+// ONCE: the rows are read past the caches (131 us otherwise).  REST: they do not end with a whole piece.
+template <class T, bool ONE, bool ONCE, bool REST>
 __global__ __launch_bounds__(kBlock) void k_combine(RowsArgs A) {
     using E = typename T::type;
-    constexpr int VE = Run16<T>::n;
+    constexpr int VE = Run16<T>::n, kAhead = kAheadMost;
     each_token<ONE>(A, [&](int64_t i, int lane, int q0, int q1) {
         const int32_t* slot = A.slot + i * A.k;
         const float* weights = A.weights ? A.weights + i * A.k : nullptr;
@@ -364,7 +362,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(RowsArgs A) {
                     const bool in = in_rows(A, s);
                     w[r] = !in ? 0.0f : weights ? weights[r0 + r] : 1.0f;
                     v[r].fill(0);
-                    if (in) v[r].get_once(static_cast<const E*>(A.in) + s * A.ld_in + j);
+                    if (in) v[r].template fetch<ONCE>(static_cast<const E*>(A.in) + s * A.ld_in + j);
                 }
 #pragma unroll
                 for (int r = 0; r < kAhead; ++r) {
@@ -375,7 +373,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(RowsArgs A) {
             }
             v[0].round(y);
             if (!REST || q < A.whole || A.apart) {
-                v[0].put_once(out + j);
+                v[0].template store<ONCE>(out + j);
             } else {
 #pragma unroll
                 for (int c = 1; c < VE; ++c)
@@ -394,13 +392,14 @@ __global__ __launch_bounds__(kBlock) void k_combine(RowsArgs A) {
     });
 }
 
-// d_rows[slot_r] = w_r d_y and d_w_r = <rows[slot_r], d_y>: d_y is read once per kAhead rows.  A thread reads a piece of
+// d_rows[slot_r] = w_r d_y and d_w_r = <rows[slot_r], d_y>: d_y is read once per kAhead rows, eight or four.  A thread reads a piece of
 // a row before it stores the gradient's, so that the gradient may take the rows' place.  Bound by memory: 16384 x 8 rows
 // of 2048 bf16 take 200 us, 5.7 TB/s.
-template <class T, int L>
+// Rows of less than a wave's pieces go four at a time: 65536 x 8 rows of 203 bf16 208 us with dispatch's gradient, 239 by eights.
+template <class T, int L, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_combine_grad(RowsArgs A) {
     using E = typename T::type;
-    constexpr int VE = Run16<T>::n, kWaves = L > 64 ? L / 64 : 1;
+    constexpr int VE = Run16<T>::n, kWaves = L > 64 ? L / 64 : 1, kAhead = L < 64 ? 4 : kAheadMost;
     __shared__ float part[kAhead][kWaves];
     if (blockIdx.x >= A.grid) return clear_padding<T>(A);
     int in_group = threadIdx.x / L;
@@ -428,7 +427,7 @@ __global__ __launch_bounds__(kBlock) void k_combine_grad(RowsArgs A) {
 #pragma unroll
                     for (int r = 0; r < kAhead; ++r) {
                         v[r].fill(0);
-                        if (s[r] >= 0) v[r].get_once(static_cast<const E*>(A.in) + s[r] * A.ld_in + q * VE);
+                        if (s[r] >= 0) v[r].template fetch<ONCE>(static_cast<const E*>(A.in) + s[r] * A.ld_in + q * VE);
                     }
                 }
                 float gf[VE];
@@ -507,6 +506,21 @@ void share(RowsArgs& A, int least) {
     A.pad_parts = A.counts ? std::min(16, std::max(1, 1024 / A.m)) : 0;
 }
 
+// Whether rows take whole cache lines, that no two share.
+template <class T>
+bool whole_lines(const void* p, int64_t ld, int d) {
+    const int64_t es = sizeof(typename T::type);
+    return reinterpret_cast<uintptr_t>(p) % 128 == 0 && ld * es % 128 == 0 && d * es % 128 == 0;
+}
+
+// Whether the rows that are summed are read past the caches: where no two share a line, or where rows are so long that few
+// of their lines are shared.  65536 x 8 rows of 203 bf16: the sum takes 49 us through the caches and 61 past them, 16384 x 8 of
+// 2040 122 and 107; both gradients of 300 286 and 315, of 2040 362 and 330.
+template <class T>
+bool past_caches(const RowsArgs& A) {
+    return A.pieces > 128 || whole_lines<T>(A.in, A.ld_in, A.d);
+}
+
 // Few tokens with long rows: several workgroups for each, every one with a run of pieces (1 x 8 rows of 8192 bf16: the sum
 // takes 4.7 us so, 10.5 in one workgroup).
 void split_rows(RowsArgs& A) {
@@ -530,8 +544,9 @@ template <class T>
 hipError_t dispatch(RowsArgs A, hipStream_t s) {
     share<T>(A, 4);
     split_rows(A);
-    const bool lines = reinterpret_cast<uintptr_t>(A.out) % 128 == 0 && A.ld_out * (int64_t)sizeof(typename T::type) % 128 == 0;
-    auto kernel = A.lanes < 64 ? k_dispatch<T, false, false> : lines ? k_dispatch<T, true, true> : k_dispatch<T, true, false>;
+    auto kernel = A.lanes < 64                                 ? k_dispatch<T, false, false>
+                  : whole_lines<T>(A.out, A.ld_out, A.d) ? k_dispatch<T, true, true>
+                                                               : k_dispatch<T, true, false>;
     return launch_rows(A, kernel, s);
 }
 
@@ -540,8 +555,12 @@ hipError_t combine(RowsArgs A, hipStream_t s) {
     share<T>(A, 4);
     split_rows(A);
     A.apart = A.add != A.out;
-    auto kernel = A.rest ? (A.lanes >= 64 ? k_combine<T, true, true> : k_combine<T, false, true>)
-                         : (A.lanes >= 64 ? k_combine<T, true, false> : k_combine<T, false, false>);
+    const bool once = past_caches<T>(A);
+    auto kernel = A.lanes < 64 ? (A.rest ? k_combine<T, false, false, true>
+                                  : once ? k_combine<T, false, true, false>
+                                         : k_combine<T, false, false, false>)
+                  : once       ? (A.rest ? k_combine<T, true, true, true> : k_combine<T, true, true, false>)
+                               : (A.rest ? k_combine<T, true, false, true> : k_combine<T, true, false, false>);
     return launch_rows(A, kernel, s);
 }
 
@@ -550,12 +569,15 @@ hipError_t combine_grad(RowsArgs A, hipStream_t s) {
     share<T>(A, 8);
     if (A.lanes == 128) A.lanes = 64;  // (a wave alone needs no barrier)
     if (!A.out) A.pad_parts = 0;
-    auto kernel = A.lanes == 8    ? k_combine_grad<T, 8>
-                  : A.lanes == 16 ? k_combine_grad<T, 16>
-                  : A.lanes == 32 ? k_combine_grad<T, 32>
-                  : A.lanes == 64 ? k_combine_grad<T, 64>
-                                  : k_combine_grad<T, 256>;
-    return launch_rows(A, kernel, s);
+    auto by_lanes = [&](auto once) {
+        constexpr bool O = decltype(once)::value;
+        return A.lanes == 8    ? k_combine_grad<T, 8, O>
+               : A.lanes == 16 ? k_combine_grad<T, 16, O>
+               : A.lanes == 32 ? k_combine_grad<T, 32, O>
+               : A.lanes == 64 ? k_combine_grad<T, 64, O>
+                               : k_combine_grad<T, 256, O>;
+    };
+    return launch_rows(A, past_caches<T>(A) ? by_lanes(std::true_type()) : by_lanes(std::false_type()), s);
 }
 
 // n windows of d elements, stride ld, at address p: what they span in bytes.

@@ -231,19 +231,28 @@ struct Run16 {
     }
     __device__ __forceinline__ void fill(uint32_t w) { raw = make_uint4(w, w, w, w); }
     __device__ __forceinline__ void get(const Elem* p) { __builtin_memcpy(&raw, p, 16); }
-    // The same for what this launch touches once: not to push out what the caches hold.
+    __device__ __forceinline__ void put(Elem* p) const { __builtin_memcpy(p, &raw, 16); }
+    // ONCE: what this launch touches once, past what the caches hold.
     typedef uint32_t Words __attribute__((ext_vector_type(4)));
     typedef Words AnyWords __attribute__((aligned(2)));
-    __device__ __forceinline__ void get_once(const Elem* p) {
-        const Words w = __builtin_nontemporal_load(reinterpret_cast<const AnyWords*>(p));
-        raw = make_uint4(w[0], w[1], w[2], w[3]);
+    template <bool ONCE>
+    __device__ __forceinline__ void fetch(const Elem* p) {
+        if constexpr (ONCE) {
+            const Words w = __builtin_nontemporal_load(reinterpret_cast<const AnyWords*>(p));
+            raw = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            get(p);
+        }
     }
-    __device__ __forceinline__ void put_once(Elem* p) const {
-        __builtin_nontemporal_store(Words{raw.x, raw.y, raw.z, raw.w}, reinterpret_cast<AnyWords*>(p));
+    template <bool ONCE>
+    __device__ __forceinline__ void store(Elem* p) const {
+        if constexpr (ONCE)
+            __builtin_nontemporal_store(Words{raw.x, raw.y, raw.z, raw.w}, reinterpret_cast<AnyWords*>(p));
+        else
+            put(p);
     }
     // Holds the run as it was loaded up to here: its conversions to float32, twice the registers, stay behind.
     __device__ __forceinline__ void held() { asm("" : "+v"(raw.x), "+v"(raw.y), "+v"(raw.z), "+v"(raw.w)); }
-    __device__ __forceinline__ void put(Elem* p) const { __builtin_memcpy(p, &raw, 16); }
 };
 
 // LDS written by this wave's lanes is visible to its other lanes (one wave's
