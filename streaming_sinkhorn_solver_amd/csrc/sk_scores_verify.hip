@@ -120,7 +120,7 @@ __device__ __forceinline__ Sum join(Sum a, Sum b, double c) {
 __device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draft, int lane) {
     const int64_t lowest = A.starts[0], end = A.starts[A.b], here = A.tokens[i], before = A.tokens[i > 0 ? i - 1 : 0];
     if (i < lowest || i >= end || (draft && here < 0)) return false;
-    if (i > 0 && before >= 0) return true;
+    if (i == 0 || before >= 0) return true;  // (row 0 is the first of its request, also where that starts below 0)
     // behind a row without a drafted token only a request's first row counts: a search by 64 at a time
     int64_t lo = 0, size = A.b;
     while (size > 64) {

@@ -1,0 +1,37 @@
+"""scores_verify where a request or a row lies at the border of what there is: starts outside the matrix, scores further
+apart than float32 reaches, a residual that is next to nothing; and every layout of the draw's chunks."""
+import numpy as np
+import pytest
+import torch
+
+import streaming_sinkhorn_solver_amd as sk
+from oracle import routed as oro
+from scores_cases import DEV
+from test_gpu_scores_verify import case, check, gpu, run
+
+pytestmark = pytest.mark.gpu
+
+
+# the first request's first row is row 0 of the matrix, the last one's last row is row n - 1; some are empty
+@pytest.mark.parametrize("starts", [[-2, 3], [-5, -1, 2, 9], [-3, -3, 4], [-7, 0, 5], [-9, -4], [0, 3, 40], [2, 7, 12, 30], [-1, 60], [12, 15],
+                                    [-2 ** 62, 4, 2 ** 62]])
+@pytest.mark.parametrize("m", [50, 9000])
+@pytest.mark.parametrize("draft", [True, False])
+def test_starts_outside_the_matrix(starts, m, draft):
+    n = 12
+    data, ref = case([n], m, "f32", m + len(starts), draft)
+    s, q, tokens, _, ua, _ = data
+    ss, qs, t, _, a, _ = ref
+    t[5] = t[8] = -1
+    st = np.array(starts, np.int64)
+    b = len(st) - 1
+    u = np.random.default_rng(b).random(b).astype(np.float32)
+    tokens, ua = gpu(t), ua * 0.5
+    a = a * np.float32(0.5)
+    for eps in (0.8, 0.0):
+        want = oro.verify(ss, t, np.clip(st, 0, n), a, u, qs, eps, 1.0, (np.full(n, 77), np.full(n, 77.0), np.full(n, 77.0)))
+        for byte in (0, 0x11, 0x3f, 0x7f, 0xff):  # what the workspace held does not matter
+            ws = sk.scores_verify_workspace(s.dtype, n, m, b, DEV).fill_(byte)
+            out = sk.Verified(*(torch.full((size,), 77, dtype=dtype, device=DEV) for size, dtype in
+                                ((b, torch.int32), (b, torch.int64), (n, torch.int64), (n, torch.float32), (n, torch.float32))))
+            check(sk.scores_verify(s, tokens, gpu(st), ua, gpu(u), draft=q, eps=eps, ws=ws, out=out), want, ss, eps)
