@@ -116,10 +116,10 @@ __device__ __forceinline__ Sum join(Sum a, Sum b, double c) {
     return {ref, moved(a, ref, c) + moved(b, ref, c)};
 }
 
-// Whether row i of the target (of the draft) is one that a request looks at.  All lanes of a wave, i the same in each.
-__device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, bool draft, int lane) {
-    const int64_t lowest = A.starts[0], end = A.starts[A.b], here = A.tokens[i], before = A.tokens[i > 0 ? i - 1 : 0];
-    if (i < lowest || i >= end || (draft && here < 0)) return false;
+// Whether row i is one that a request looks at.  All lanes of a wave, i the same in each.
+__device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, int lane) {
+    const int64_t lowest = A.starts[0], end = A.starts[A.b], before = A.tokens[i > 0 ? i - 1 : 0];
+    if (i < lowest || i >= end) return false;
     if (i == 0 || before >= 0) return true;  // (row 0 is the first of its request, also where that starts below 0)
     // behind a row without a drafted token only a request's first row counts: a search by 64 at a time
     int64_t lo = 0, size = A.b;
@@ -162,8 +162,9 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
 #pragma unroll
             for (int q = 0; q < NV; ++q) next[q].get(row + (int64_t)min(v0 + b * kStep + q * kThreads + t, v1 - 1) * VE);
         };
-        if (blocks > 0) fetch(0);  // (before it is known whether the row counts)
-        if (!row_counts(A, i, draft, lane)) continue;
+        if (draft && A.tokens[i] < 0) continue;  // (such a row of the draft need not be there)
+        if (blocks > 0) fetch(0);                // (before it is known whether the row counts)
+        if (!row_counts(A, i, lane)) continue;
         float M = kNegBig, S = 0.0f;  // (M starts above -inf)
         if (split == 0 && t < tail) {
             const float x = T::to(row[runs * VE + t]);
@@ -650,7 +651,7 @@ __global__ __launch_bounds__(kBlock) void k_verify_best(VfArgs A) {
     uint64_t* best_of = reinterpret_cast<uint64_t*>(A.sums);
     const int split = (int)blockIdx.y;
     for (int64_t i = (int64_t)blockIdx.x * kRows + slot; i < A.n; i += (int64_t)gridDim.x * kRows) {
-        if (!row_counts(A, i, false, lane)) continue;
+        if (!row_counts(A, i, lane)) continue;
         const E* row = static_cast<const E*>(A.s) + i * A.ld;
         const int runs = A.m / VE, tail = A.m - runs * VE;
         const int v0 = split * A.cut, v1 = min(runs, v0 + A.cut);

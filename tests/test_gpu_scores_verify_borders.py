@@ -35,3 +35,24 @@ def test_starts_outside_the_matrix(starts, m, draft):
             out = sk.Verified(*(torch.full((size,), 77, dtype=dtype, device=DEV) for size, dtype in
                                 ((b, torch.int32), (b, torch.int64), (n, torch.int64), (n, torch.float32), (n, torch.float32))))
             check(sk.scores_verify(s, tokens, gpu(st), ua, gpu(u), draft=q, eps=eps, ws=ws, out=out), want, ss, eps)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [40, 3000, 20000])
+def test_draft_rows_that_are_not_there(m, dtype):
+    """Rows of the draft without a drafted token are not read: the matrix may end before the last request's last row."""
+    data, ref = case([3, 2, 1, 4], m, dtype, m, True)
+    s, q, tokens, starts, ua, us = data
+    n, b = s.shape[0], 4
+    want = sk.scores_verify(s, tokens, starts, ua, us, draft=q)
+    short = torch.full((n - 1, m), float("nan"), dtype=q.dtype, device=DEV)
+    rows = (tokens >= 0).nonzero()[:, 0]
+    short[rows] = q[rows]
+    out = [torch.empty_like(t) for t in want]
+    ws = sk.scores_verify_workspace(s.dtype, n, m, b, DEV)
+    code = sk.load_library().sk_scores_verify(
+        s.data_ptr(), sk.DTYPES[s.dtype], n, m, s.stride(0), 1.0, short.data_ptr(), m, 1.0, tokens.data_ptr(), starts.data_ptr(), b,
+        ua.data_ptr(), us.data_ptr(), *(t.data_ptr() for t in out), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    for got, ref_ in zip(out, want):
+        assert torch.equal(got, ref_)
