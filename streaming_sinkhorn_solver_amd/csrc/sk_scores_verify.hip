@@ -57,7 +57,8 @@ struct VfArgs {
     int64_t ld, ldq, n, b;
     int m;
     double c, cq;    // log2e / eps
-    float cf, cqf;   // the same in float32
+    float cf, cqf;   // in float32: c over scale
+    float scale, scale_q;  // of the scores before their differences: 1, or 1/2 at temperatures where one beyond float32 counts
     double doubt;    // relative error of p / q from the float32 sums at most
     const int64_t *tokens, *starts;
     const float *u_accept, *u_sample;
@@ -135,8 +136,10 @@ __device__ __forceinline__ bool row_counts(const VfArgs& A, int64_t i, int lane)
     return __ballot(lane < size && A.starts[min(lo + lane, A.b)] == i) != 0;
 }
 
+// 2^(c (x - top)) with the difference taken of the scaled values (exact products: one rounding, that of the difference).
+__device__ __forceinline__ float ex2_below(float x, float top, float scale, float c) { return s_ex2(fmaf(x, scale, -(top * scale)) * c); }
 // S for the reference M to the same for top >= M.
-__device__ __forceinline__ float rescaled(float S, float M, float top, float c) { return S * s_ex2((M - top) * c); }
+__device__ __forceinline__ float rescaled(float S, float M, float top, float scale, float c) { return S * ex2_below(M, top, scale, c); }
 
 // Sums of the rows' exponentials in float32: a row, or a part of one, per W waves, each thread with a running maximum
 // that it moves once per kVfVecs loads.  (A NaN or +inf score makes the sum NaN by itself.)  Bound by memory: 512 rows
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
     // the grid's second dimension: parts of a row, of the target's and then of the draft's
     const int kind = blockIdx.y >= (unsigned)A.splits, split = (int)blockIdx.y - kind * A.splits;
     const bool draft = kind == 1;
-    const float c = draft ? A.cqf : A.cf;
+    const float c = draft ? A.cqf : A.cf, scale = draft ? A.scale_q : A.scale;
     for (int64_t i = (int64_t)blockIdx.x * kRows + slot; i < A.n; i += (int64_t)gridDim.x * kRows) {
         const E* row = static_cast<const E*>(draft ? A.q : A.s) + i * (draft ? A.ldq : A.ld);
         const int runs = A.m / VE, tail = A.m - runs * VE;
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
         if (split == 0 && t < tail) {
             const float x = T::to(row[runs * VE + t]);
             M = fmaxf(M, x);
-            S = s_ex2((x - M) * c);
+            S = ex2_below(x, M, scale, c);
         }
         for (int b = 0; b < blocks; ++b) {
 #pragma unroll
@@ -186,13 +189,13 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
             for (int q = 0; q < NV; ++q)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) top = fmaxf(top, v[q].at(e));
-            S = rescaled(S, M, top, c);
+            S = rescaled(S, M, top, scale, c);
             M = top;
             float s = 0.0f;
 #pragma unroll
             for (int q = 0; q < NV; ++q)
 #pragma unroll
-                for (int e = 0; e < VE; ++e) s += s_ex2((v[q].at(e) - M) * c);
+                for (int e = 0; e < VE; ++e) s += ex2_below(v[q].at(e), M, scale, c);
             S += s;
         }
         float top = lanes_max<64>(M);
@@ -203,7 +206,7 @@ __global__ __launch_bounds__(kBlock) void k_verify_sums(VfArgs A) {
 #pragma unroll
             for (int w = 0; w < W; ++w) top = fmaxf(top, red[w][0]);
         }
-        S = lanes_sum<64>(rescaled(S, M, top, c));
+        S = lanes_sum<64>(rescaled(S, M, top, scale, c));
         if (W > 1) {
             if (lane == 0) red[wave][1] = S;
             __syncthreads();
@@ -846,8 +849,10 @@ int sk_scores_verify(const void* scores, int32_t dtype, int64_t n, int64_t m, in
     A.m = (int)m;
     A.c = greedy ? 1.0 : 1.4426950408889634074 / (double)eps;
     A.cq = draft ? 1.4426950408889634074 / (double)eps_draft : 1.0;
-    A.cf = (float)A.c;
-    A.cqf = (float)A.cq;
+    A.scale = A.c < 1.0 ? 0.5f : 1.0f;  // (from c = 1 on, twice c may leave float32, and an infinite difference is none that counts)
+    A.scale_q = A.cq < 1.0 ? 0.5f : 1.0f;
+    A.cf = (float)(A.c / A.scale);
+    A.cqf = (float)(A.cq / A.scale_q);
     // the float32 sums: an exponent carries 3 u of itself, and as much again by the moves of the maximum, of which the
     // weighted mean is at most ln m; 2 u the exponential; then the additions of a block, of the blocks (with 3 u for each
     // move), lanes and waves

@@ -56,3 +56,25 @@ def test_draft_rows_that_are_not_there(m, dtype):
     assert code == 0
     for got, ref_ in zip(out, want):
         assert torch.equal(got, ref_)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [2, 5, 600, 30000])
+@pytest.mark.parametrize("draft", [True, False])
+def test_scores_further_apart_than_float32_reaches(m, dtype, draft):
+    """Differences of scores beyond the largest float32, at temperatures where they count."""
+    data, ref = case([3, 2, 4, 1], m, dtype, m, draft)
+    s, q, ss, qs = data[0], data[1], ref[0], ref[1]
+    r = np.random.default_rng(m)
+    for i in range(10):
+        for win, held in ((s, ss), (q, qs)):
+            if win is None:
+                continue
+            x = r.choice([-3e38, 3e38, -2e38, 1e38, 0.0], m)
+            x[r.integers(m)] = -3e38 if i % 2 else 3e38  # (a thread's first scores far below or above the others)
+            win[i] = gpu(x).to(win.dtype)
+            held[i] = win[i].double().cpu().numpy()
+    for eps in (1e38, 3e37, 5e36):
+        run(data, ref, eps=eps, eps_draft=eps)
+        run(data, ref, eps=eps, eps_draft=1.2e38)
+    run(data, ref, eps=1.0, eps_draft=1e-30)
