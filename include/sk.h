@@ -596,8 +596,8 @@ int sk_scores_logprobs_grad(const void *scores, int32_t dtype, int64_t n, int64_
  * too, makes its row's ratio NaN (not taken) and nothing is drawn there.  ratio and logp
  * come from float32 sums; a decision that these leave open, and every draw, is taken in
  * float64 (probabilities below 2^-900 count as 0), so that they are those of the exact
- * probabilities but within some 2^-38 of a border (a draw within 2^-22 where p and q are
- * proportional over much of the row and their sums differ by less than that).
+ * probabilities but within some 2^-38 of a border; p - q leaves nothing where its sum is 2^-40
+ * or less.
  */
 size_t sk_scores_verify_workspace_bytes(int32_t dtype, int64_t n, int64_t m, int64_t b);
 int sk_scores_verify(const void *scores, int32_t dtype, int64_t n, int64_t m, int64_t ld,

@@ -16,10 +16,11 @@
 // exponentials of p's and q's row and rho the quotient of their sums, the residual is
 // max(e - rho h, 0).  One pass takes sum e and sum h, which give rho, and with rho0 from the
 // float32 sums R = sum max(e - rho0 h, 0) and B = sum of h where e > rho0 h.  The residual's
-// sum is then R + (rho0 - rho) B but for entries whose e / h lies between the two quotients,
-// some 2^-22 apart: each is off by that share of itself, and in general they are that share of
-// all.  (Were p and q proportional over much of the row, their sums alike to 2^-22 and yet
-// not equal, a draw would be exact to that distance of a border only.)
+// sum is then R + (rho0 - rho) B but for entries whose e / h lies between the two quotients:
+// each is off by |rho0 - rho| h at most, some 2^-22 of itself, and must lie within the bound
+// of the float32 error of rho0 (2^-15 to 2^-17), where the pass leaves a mark on its chunk.  A
+// draw that is nearer to a border than these errors can add up to has the marked chunks summed
+// again with rho itself: few draws, but many where p and q are proportional over much of the row.
 #include "sk_scores.hpp"
 
 #include <algorithm>
@@ -59,6 +60,7 @@ struct VfArgs {
     double c, cq;    // log2e / eps
     float cf, cqf;   // in float32: c over scale
     float scale, scale_q;  // of the scores before their differences: 1, or 1/2 at temperatures where one beyond float32 counts
+    double floor, floor_q;  // kFloor / c
     double doubt;    // relative error of p / q from the float32 sums at most
     const int64_t *tokens, *starts;
     const float *u_accept, *u_sample;
@@ -369,34 +371,49 @@ __device__ Draw look(const VfArgs& A, int64_t r, bool write, Look& L) {
     return d;
 }
 
+// The same in scalar registers; all threads have the same.
+__device__ __forceinline__ Draw uniform(const Draw& d) {
+    struct Words {
+        int w[sizeof(Draw) / 4];
+    };
+    Words x = __builtin_bit_cast(Words, d);
+#pragma unroll
+    for (int& w : x.w) w = __builtin_amdgcn_readfirstlane(w);
+    return __builtin_bit_cast(Draw, x);
+}
+
 __device__ __forceinline__ bool drawable(const Draw& d) {
     return d.row >= 0 && d.log_p > -(double)INFINITY && (!d.with_q || d.rho == d.rho);  // (NaN: no)
 }
 
-// The exponential of a score over its row's largest: 0 below the floor; or, where that is told apart later, 2^-1000.
-__device__ __forceinline__ double exp_of(float s, double ref, double c) { return pow2_or_zero(((double)s - ref) * c); }
+// The exponential of a score over its row's largest, floor / c below it: 2^-1000, where that is told apart later; or 0.
 __device__ __forceinline__ double exp_near(float s, double ref, double c, double floor) {
     return pow2(fmax((double)s - ref, floor), c);
 }
+__device__ __forceinline__ double exp_of(float s, double ref, double c, double floor) {
+    return (double)s - ref > floor ? exp_near(s, ref, c, floor) : 0.0;
+}
 
-// Sums over a chunk, by a wave: of e, of h, of max(e - rho h, 0) and of h where that is positive (without q: of e).
+// Sums over a chunk, by a wave: of e, of h, of max(e - rho h, 0) and of h where that is positive (without q: of e).  With
+// near > 0 the second is negative where an entry has |e - rho h| <= near h.
 template <class T>
-__device__ __forceinline__ void chunk_sums(const VfArgs& A, const Draw& d, int chunk, int lane, double* out) {
+__device__ __forceinline__ void chunk_sums(const VfArgs& A, const Draw& d, double near, int chunk, int lane, double* out) {
     using E = typename T::type;
     constexpr int VE = Run16<T>::n;
     const int start = chunk * A.chunk_len, j0 = start + lane * VE, size = min(A.chunk_len, A.m - start);
     const E* s = static_cast<const E*>(A.s) + d.row * A.ld + j0;
     const E* q = static_cast<const E*>(d.with_q ? A.q : A.s) + d.row * (d.with_q ? A.ldq : A.ld) + j0;
-    const double floor = kFloor / A.c, floor_q = kFloor / A.cq;
-    double e = 0.0, h = 0.0, rest = 0.0, hot = 0.0;
+    double e = 0.0, h = 0.0, rest = 0.0, hot = 0.0, gap = 1.0;
     auto add_both = [&](float x, float y) {
-        const double a = exp_near(x, d.ref_p, A.c, floor), b = exp_near(y, d.ref_q, A.cq, floor_q), w = fma(-d.rho, b, a);
+        const double a = exp_near(x, d.ref_p, A.c, A.floor), b = exp_near(y, d.ref_q, A.cq, A.floor_q), w = fma(-d.rho, b, a);
         e += a;
         h += b;
-        rest += fmax(w, 0.0);
-        hot += w > 0.0 ? b : 0.0;
+        const double over = fmin(fmax(w * 0x1p1020, 0.0), 1.0);  // 1 where w > 0 (one instruction, where a choice takes three)
+        rest = fma(w, over, rest);
+        hot = fma(b, over, hot);
+        gap = fmin(gap, fma(-near, b, fabs(w)));
     };
-    auto add_one = [&](float x, int j) { e += j == d.out ? 0.0 : exp_near(x, d.ref_p, A.c, floor); };
+    auto add_one = [&](float x, int j) { e += j == d.out ? 0.0 : exp_near(x, d.ref_p, A.c, A.floor); };
     const int whole = size / (64 * VE) * (64 * VE);  // entries in whole runs of all lanes
     // (the loops are not unrolled: a wave has few chunks, and cold code takes longer to fetch than to run)
     if (d.with_q) {
@@ -440,6 +457,7 @@ __device__ __forceinline__ void chunk_sums(const VfArgs& A, const Draw& d, int c
     double x = odd ? x1 : x0;
     x += __shfl_xor(odd ? x0 : x1, 16);
     for (int o = 8; o > 0; o /= 2) x += __shfl_xor(x, o);
+    if (near > 0.0 && __any(gap <= 0.0) && lane / 16 == 1) x = -x;
     if ((lane & 15) == 0) out[lane / 16] = x;
 }
 
@@ -463,8 +481,20 @@ __device__ __forceinline__ double block_scan(double x, double* lds, double& tota
     return before + x;
 }
 
+// Sums of x and of y over the workgroup's threads, the same in every thread.
+__device__ __forceinline__ void block_sums(double x, double y, double (*lds)[2], double& sum_x, double& sum_y) {
+    x = lanes_sum<64>(x);
+    y = lanes_sum<64>(y);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x / 64][0] = x, lds[threadIdx.x / 64][1] = y;
+    __syncthreads();
+    sum_x = sum_y = 0.0;
+#pragma unroll
+    for (int w = 0; w < kBlock / 64; ++w) sum_x += lds[w][0], sum_y += lds[w][1];
+}
+
 struct Pick {
-    double scan[kBlock / 64], prior;
+    double scan[kBlock / 64], two[kBlock / 64][2], prior, room;
     uint64_t over[kBlock / 64], some[kBlock / 64];
 };
 
@@ -486,40 +516,53 @@ __device__ __forceinline__ int first_over(bool over, bool some, Pick& L, bool& f
     return found ? first : last;
 }
 
-// The draw of a request from its chunks' sums, by a whole workgroup.
+// The draw of a request from its chunks' sums, by a whole workgroup.  False where it is nearer to a border than the marked
+// chunks' sums allow: they are to be taken again, with rho; after that (exact) they are as good as the others.
 template <class T>
-__device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
+__device__ bool draw(const VfArgs& A, int64_t r, Draw d, bool exact, double& rho, Pick& L) {
     using E = typename T::type;
     constexpr int kPer = kVfChunkMost / kBlock;
     const int tid = threadIdx.x;
     const double* sums = A.chunk + r * A.chunks * 4;
     if (tid == 0) A.out_tokens[d.row] = -1;  // (until the draw)
     double shift = 0.0, all = 0.0;  // rho0 - rho; the sum of e
+    double slack = 0.0;             // what a sum of chunks' weights is off by at most
     if (d.with_q) {
         double h = 0.0;
         for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
             const int k = k0 + tid;
-            double here;
-            block_scan(k < A.chunks ? sums[4 * k] : 0.0, L.scan, here);
-            all += here;
-            block_scan(k < A.chunks ? sums[4 * k + 1] : 0.0, L.scan, here);
-            h += here;
+            double e_here, h_here;
+            block_sums(k < A.chunks ? sums[4 * k] : 0.0, k < A.chunks ? fabs(sums[4 * k + 1]) : 0.0, L.two, e_here, h_here);
+            all += e_here;
+            h += h_here;
         }
         shift = d.rho - all / h;
-        d.rho = all / h;
+        rho = d.rho = all / h;
+        slack = exact ? 0.0 : fabs(shift) * h;
     }
+    double mine = 0.0, upto = 0.0, here, total = 0.0;
     auto weight_of = [&](int k) {
         if (k >= A.chunks) return 0.0;
         const double w = d.with_q ? fma(shift, sums[4 * k + 3], sums[4 * k + 2]) : sums[4 * k];
         return w > kNothing ? w : 0.0;
     };
-    double mine = 0.0, upto = 0.0, here, total = 0.0;
+    // only the marked chunks' weights are off
+    auto sum_marked = [&]() {
+        double h = 0.0;
+        for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
+            const double marked = k0 + tid < A.chunks ? fmax(-sums[4 * (k0 + tid) + 1], 0.0) : 0.0;
+            block_scan(marked, L.scan, here);
+            h += here;
+        }
+        slack = fabs(shift) * h;
+    };
     for (int k0 = 0; k0 < A.chunks; k0 += kBlock) {
         mine = weight_of(k0 + tid);
         upto = block_scan(mine, L.scan, here);
         total += here;
     }
-    if (d.with_q && !(total > 0x1p-40 * all)) {
+    if (d.with_q && !(total - slack > 0x1p-40 * all)) {
+        if (slack > 0.0) return false;
         // p - q leaves nothing (q = p, but for roundings): the draw is from p itself
         d.with_q = 0;
         total = all;
@@ -534,10 +577,10 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
             A.next[r] = A.out_tokens[d.row] = d.out;
             A.logp[d.row] = 0.0f;
         }
-        return;
+        return true;
     }
-    // the first chunk whose sum with those before exceeds the mark; where none does (u_sample = 1), the last whose sum is
-    // more than roundings
+    // the first chunk whose sum with those before exceeds the mark; where none does (u_sample = 1), the last whose sum
+    // is more than roundings
     const double mark = (double)fminf(fmaxf(A.u_sample[r], 0.0f), 1.0f) * total;
     int at = -1;
     double before = 0.0;
@@ -575,25 +618,40 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
                 b[e] = t[min(j0 + e, end - 1)];
             }
         }
+        // (as in the chunk's sums: what counts there counts here)
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const double p = j0 + e == d.out ? 0.0 : exp_of(T::to(a[e]), d.ref_p, A.c);
-            const double q = d.with_q ? exp_of(T::to(b[e]), d.ref_q, A.cq) : 0.0;
+            const double p = j0 + e == d.out ? 0.0 : exp_of(T::to(a[e]), d.ref_p, A.c, A.floor);
+            const double q = d.with_q ? exp_of(T::to(b[e]), d.ref_q, A.cq, A.floor_q) : 0.0;
             w[e] = j0 + e < end ? fmax(fma(-d.rho, q, p), 0.0) : 0.0;
             mine += w[e];
         }
     }
-    double run = prior + (block_scan(mine, L.scan, here) - mine);
+    double run = prior + (block_scan(mine, L.scan, here) - mine), room = -1.0;
     int first = -1, possible = -1;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
+        const double below = run;
         run += w[e];
         if (w[e] > 0.0) {
             possible = j0 + e;
-            if (run > mark && first < 0) first = j0 + e;
+            if (run > mark && first < 0) {
+                first = j0 + e;
+                room = fmin(mark - below, run - mark);
+            }
         }
     }
     const int hit = first_over(first >= 0, possible >= 0, L, found);
+    if (slack > 0.0) {
+        // the distance to the nearest border against what the mark and the sum before may be off by
+        if (tid == hit) L.room = room;
+        __syncthreads();
+        const double least = hit < 0 ? -1.0 : L.room;
+        if (!(least > 2.0 * slack)) {
+            sum_marked();
+            if (slack > 0.0 && !(least > 2.0 * slack)) return false;
+        }
+    }
     if (tid == hit) {
         const int token = found ? first : possible;  // (roundings: the last possible entry of the chunk)
         A.next[r] = token;
@@ -601,30 +659,38 @@ __device__ void draw(const VfArgs& A, int64_t r, Draw d, Pick& L) {
         A.logp[d.row] = (float)(column_log(T::to(s[token]), A.c, {d.ref_p, d.log_p}) * 0.6931471805599453094);
     }
     __syncthreads();
+    return true;
 }
 
 // Where each request stops and the sums of the chunks of what it draws from: a wave per chunk, A.parts workgroups per
-// request; one that has all the chunks draws too.  Bound by the issue of some 40 float64 instructions per entry: 64
+// request; one that has all the chunks (ALONE) draws too.  Bound by the issue of some 40 float64 instructions per entry: 64
 // requests over 131072 columns take 22 us, 5 of them to look where each stops.
-template <class T>
+template <class T, bool ALONE>
 __global__ __launch_bounds__(kBlock, 4) void k_verify_chunks(VfArgs A) {
     __shared__ Look L;
-    __shared__ Pick P;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     for (int64_t item = blockIdx.x; item < A.b * A.parts; item += gridDim.x) {
         const int64_t r = item / A.parts;
         const int part = (int)(item % A.parts);
-        const Draw d = look<T>(A, r, part == 0, L);
-        if (A.parts > 1 && part == 0 && threadIdx.x == 0) A.draw[r] = d;
-        if (drawable(d))
+        Draw d = uniform(look<T>(A, r, part == 0, L));
+        if (!ALONE && part == 0 && threadIdx.x == 0) A.draw[r] = d;
+        if (!drawable(d)) {
+            if (ALONE && d.row >= 0 && threadIdx.x == 0) A.out_tokens[d.row] = -1;
+            continue;
+        }
+        for (double near = A.doubt * d.rho;; near = 0.0) {
             for (int k = part * (kBlock / 64) + wave; k < A.chunks; k += A.parts * (kBlock / 64))
-                chunk_sums<T>(A, d, k, lane, A.chunk + (r * A.chunks + k) * 4);
-        if (A.parts > 1) continue;
-        __syncthreads();
-        if (drawable(d))
-            draw<T>(A, r, d, P);
-        else if (d.row >= 0 && threadIdx.x == 0)
-            A.out_tokens[d.row] = -1;
+                chunk_sums<T>(A, d, near, k, lane, A.chunk + (r * A.chunks + k) * 4);
+            if constexpr (ALONE) {
+                __shared__ Pick P;
+                __syncthreads();
+                double rho = d.rho;
+                if (draw<T>(A, r, d, near == 0.0, rho, P)) break;
+                d.rho = rho;  // (all chunks again)
+            } else {
+                break;
+            }
+        }
     }
 }
 
@@ -632,12 +698,25 @@ __global__ __launch_bounds__(kBlock, 4) void k_verify_chunks(VfArgs A) {
 template <class T>
 __global__ __launch_bounds__(kBlock) void k_verify_draw(VfArgs A) {
     __shared__ Pick P;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     for (int64_t r = blockIdx.x; r < A.b; r += gridDim.x) {
-        const Draw d = A.draw[r];
-        if (drawable(d))
-            draw<T>(A, r, d, P);
-        else if (d.row >= 0 && threadIdx.x == 0)
-            A.out_tokens[d.row] = -1;
+        const Draw d = uniform(A.draw[r]);
+        if (!drawable(d)) {
+            if (d.row >= 0 && threadIdx.x == 0) A.out_tokens[d.row] = -1;
+            continue;
+        }
+        double* sums = A.chunk + r * A.chunks * 4;
+        Draw again = d;
+        for (bool exact = false; !draw<T>(A, r, d, exact, again.rho, P); exact = true) {
+            // the marked chunks, which need no correction then
+            __syncthreads();
+            for (int k = wave; k < A.chunks; k += kBlock / 64) {
+                if (!(sums[4 * k + 1] < 0.0)) continue;
+                chunk_sums<T>(A, again, 0.0, k, lane, sums + 4 * k);
+                if (lane == 48) sums[4 * k + 3] = 0.0;  // (the lane that wrote it)
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -800,7 +879,8 @@ hipError_t verify(const VfArgs& A, bool greedy, hipStream_t s) {
     else
         hipLaunchKernelGGL((k_verify_sums<T, 4>), grid, dim3(kBlock), 0, s, A);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((k_verify_chunks<T>), dim3((unsigned)std::min<int64_t>(A.b * A.parts, kVfGrid)), dim3(kBlock), 0, s, A);
+    auto chunks = A.parts == 1 ? k_verify_chunks<T, true> : k_verify_chunks<T, false>;
+    hipLaunchKernelGGL(chunks, dim3((unsigned)std::min<int64_t>(A.b * A.parts, kVfGrid)), dim3(kBlock), 0, s, A);
     if ((e = hipGetLastError()) != hipSuccess || A.parts == 1) return e;
     hipLaunchKernelGGL((k_verify_draw<T>), dim3((unsigned)std::min<int64_t>(A.b, kVfGrid)), dim3(kBlock), 0, s, A);
     return hipGetLastError();
@@ -849,6 +929,8 @@ int sk_scores_verify(const void* scores, int32_t dtype, int64_t n, int64_t m, in
     A.m = (int)m;
     A.c = greedy ? 1.0 : 1.4426950408889634074 / (double)eps;
     A.cq = draft ? 1.4426950408889634074 / (double)eps_draft : 1.0;
+    A.floor = kFloor / A.c;
+    A.floor_q = kFloor / A.cq;
     A.scale = A.c < 1.0 ? 0.5f : 1.0f;  // (from c = 1 on, twice c may leave float32, and an infinite difference is none that counts)
     A.scale_q = A.cq < 1.0 ? 0.5f : 1.0f;
     A.cf = (float)(A.c / A.scale);

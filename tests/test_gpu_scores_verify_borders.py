@@ -78,3 +78,50 @@ def test_scores_further_apart_than_float32_reaches(m, dtype, draft):
         run(data, ref, eps=eps, eps_draft=eps)
         run(data, ref, eps=eps, eps_draft=1.2e38)
     run(data, ref, eps=1.0, eps_draft=1e-30)
+
+
+def next_to_proportional(m, seed, off):
+    """A target's and a draft's row whose probabilities are alike but for one column in 512 that the target raises by some
+    2^-28 each, and a drafted one that it lowers so far that the sums differ by `off` of what was added.  The draft's
+    scores are 1.5 times as large, at 1.5 times the temperature, so float32 sums of the two differ by roundings."""
+    r = np.random.default_rng(seed)
+    base = np.round(r.normal(size=m) * 32) / 16
+    top = base.max()
+    first = np.arange(0, m, 512)
+    up = first + r.integers(0, 1 << 30, len(first)) % np.minimum(512, m - first)
+    base[up] = top - 16 - np.round(r.random(len(up)) * 16) / 16
+    added = (np.exp(base[up] - top) * (np.e - 1)).sum()
+    down = (up[0] + 1) % m
+    base[down] = np.round(16 * (top + np.log(4 * added))) / 16
+    s = base.astype(np.float32)
+    s[up] += 1
+    s[down] = np.float32(top + np.log(np.exp(base[down] - top) - added * (1 - off)))
+    return s, (1.5 * base).astype(np.float32), down
+
+
+@pytest.mark.parametrize("off", [0.5, 0.1, 0.02, 0.0, -0.1, -0.5, -2.0])
+@pytest.mark.parametrize("m,b", [(20000, 4), (20000, 512), (700, 1200), (140000, 6)])
+def test_residual_next_to_nothing(m, b, off):
+    """The draw is that of the exact residual also where p and q are alike in nearly all of the row and what is left is 2^-21 or
+    less.  An exponential is within 2^-38 of itself, and in a column where p and q are alike both carry the same error, so
+    borders are within some 2^-17 of what is left; the random numbers keep 2^-13 away from every one."""
+    kinds = 4
+    rows = [next_to_proportional(m, 10 * k + m, off) for k in range(kinds)]
+    r = np.random.default_rng(b)
+    s, q, tokens = np.zeros((2 * b, m), np.float32), np.zeros((2 * b, m), np.float32), np.full(2 * b, -1, np.int64)
+    us, want = np.zeros(b, np.float32), np.zeros(b, np.int64)
+    for k, (target, draft, down) in enumerate(rows):
+        w = np.maximum(oro.distribution(target, 1.0)[0] - oro.distribution(draft, 1.5)[0], 0.0)
+        w /= w.sum()
+        ends = np.cumsum(w)
+        heavy = np.nonzero(w > 2.0 ** -11)[0]
+        for i in range(k, b, kinds):
+            j = int(r.choice(heavy))
+            us[i] = ends[j] - w[j] * r.uniform(0.3, 0.7)
+            if off > 0.0 and i < 2 * kinds and i % 2:  # (only the raised columns are left)
+                j, us[i] = int(np.nonzero(w)[0][0]), 0.0
+            s[2 * i], q[2 * i], tokens[2 * i], want[i] = target, draft, down, j
+    got = sk.scores_verify(gpu(s), gpu(tokens), gpu(2 * np.arange(b + 1)), torch.full((2 * b,), 0.97, device=DEV), gpu(us),
+                           draft=gpu(q), eps=1.0, eps_draft=1.5)
+    assert (got.accepted == 0).all()
+    assert np.array_equal(got.next.cpu().numpy(), want)
