@@ -1,0 +1,34 @@
+"""The routed rows' sort at every number of pairs of a thread, and their buffers: windows of one buffer, outputs that
+change apart from one another."""
+import numpy as np
+import pytest
+import torch
+
+import streaming_sinkhorn_solver_amd as sk
+from scores_cases import DEV, DTYPES
+
+pytestmark = pytest.mark.gpu
+
+
+# the pairs of a thread are 1, 2, 4, 8 or 16, by the pairs that one workgroup (up to 4096) or the most of them would leave
+@pytest.mark.parametrize("align,capacity", [(1, 0), (16, 0), (4, 90)])
+@pytest.mark.parametrize("n,k,m", [(2047, 1, 1000), (4095, 1, 70), (99, 41, 1000), (9091, 11, 1000), (28571, 7, 1000), (400001, 1, 1000), (524287, 1, 1000),
+                                   (157143, 7, 1000), (74899, 7, 60), (131071, 8, 60), (350003, 6, 60), (65535, 9, 512)])
+def test_sort_pairs_of_a_thread(n, k, m, align, capacity):
+    """Several workgroups, the last with fewer pairs, for every number of pairs of a thread."""
+    r = np.random.default_rng(n)
+    idx = r.integers(-m // 8, m + m // 8, (n, k)).astype(np.int32)  # (a fifth is none of the experts)
+    plan = sk.route_sort(torch.from_numpy(idx).to(DEV), m, align=align, capacity=capacity)
+    flat = idx.reshape(-1).astype(np.int64)
+    flat = np.where((flat >= 0) & (flat < m), flat, m)
+    order = np.argsort(flat, kind="stable")
+    every = np.bincount(flat, minlength=m + 1)
+    rank = np.arange(n * k) - (np.cumsum(every) - every)[flat[order]]
+    kept = (flat[order] < m) & ((rank < capacity) if capacity else True)
+    counts = np.minimum(every[:m], capacity) if capacity else every[:m]
+    offsets = np.concatenate([[0], np.cumsum(-(-counts // align) * align)])
+    slot, source = np.full(n * k, -1), np.full(plan.source.numel(), -1)
+    slot[order[kept]] = offsets[flat[order[kept]]] + rank[kept]
+    source[slot[order[kept]]] = order[kept]
+    for got, want in zip(plan, (slot.reshape(n, k), source, counts, offsets)):
+        assert np.array_equal(got.cpu().numpy(), want)

@@ -125,3 +125,39 @@ def test_residual_next_to_nothing(m, b, off):
                            draft=gpu(q), eps=1.0, eps_draft=1.5)
     assert (got.accepted == 0).all()
     assert np.array_equal(got.next.cpu().numpy(), want)
+
+
+# A chunk of the draw is 512 entries where b m is 2^21 at most, 1024 up to 2^22, 2048 beyond.  Up to 256 chunks are added up
+# by the threads at once, more in turns; with 1024 requests or more a request's chunks are one workgroup's.
+LAYOUTS = [([4], 131072), ([4], 131073), ([3, 1], 151936), ([2], 201089), ([2], 262144), ([2], 600011),  # 512, 256 chunks and more
+           ([2] * 60, 43008), ([2] * 60, 43007), ([2] * 50, 46081),                                       # 1024
+           ([2] * 120, 40961), ([2] * 120, 40960), ([2, 1] * 9, 270337),                                  # 2048
+           ([2] * 1100, 9001), ([1, 2] * 600, 513)]                                                       # a workgroup per request
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("lengths,m", LAYOUTS, ids=lambda v: f"{len(v)}x{v[0]}" if isinstance(v, list) else str(v))
+def test_layouts_of_the_draw(lengths, m, draft, dtype):
+    data, ref = case(lengths, m, dtype, m, draft)
+    b, r = len(lengths), np.random.default_rng(m)
+    below = np.nextafter(np.float32(1), np.float32(0))
+    run(data, ref)
+    # what is drawn at the ends and in the middle of the row, also where all drafted tokens but the last are taken
+    for u in ((0.0, below, 0.5) if b < 4 else (np.where(r.random(b) < 0.5, 0.0, below),)):
+        a, u = np.where(r.random(len(ref[4])) < 0.5, below, 0.0).astype(np.float32), np.broadcast_to(u, b).astype(np.float32)
+        run(data[:4] + (gpu(a), gpu(u)), ref[:4] + (a, u))
+
+
+@pytest.mark.parametrize("m,b", [(9001, 2), (9001, 1100), (131073, 3), (151936, 3), (50001, 64)])
+def test_nothing_left_to_draw_from(m, b):
+    """p = q and a drafted token that is refused all the same: the draw is from p; also in a row whose mass is at its ends."""
+    data, ref = case([2] * b, m, "f32", b, True)
+    s, ss = data[0], ref[0]
+    s[:2, 1:m - 1] = -float("inf")
+    ss[:2, 1:m - 1] = -np.inf
+    a = np.ones(2 * b, np.float32)
+    t = ref[2].copy()
+    t[0] = 0
+    got = run((s, s, gpu(t), data[3], gpu(a), data[5]), (ss, ss, t, ref[3], a, ref[5]))
+    assert (got.accepted == 0).all() and (got.next >= 0).all()
