@@ -580,15 +580,21 @@ hipError_t combine_grad(RowsArgs A, hipStream_t s) {
     return launch_rows(A, past_caches<T>(A) ? by_lanes(std::true_type()) : by_lanes(std::false_type()), s);
 }
 
-// n windows of d elements, stride ld, at address p: what they span in bytes.
+// Rows of d elements, stride ld, at address p.
 struct Span {
-    uintptr_t lo, hi;
+    uintptr_t lo, hi, row, width;  // in bytes: what they span, the stride, a row
 };
 Span span_of(const void* p, int64_t n, int64_t d, int64_t ld, int es) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, n > 0 ? a + (uintptr_t)(((n - 1) * ld + d) * es) : a};
+    return {a, n > 0 ? a + (uintptr_t)(((n - 1) * ld + d) * es) : a, (uintptr_t)(ld * es), (uintptr_t)(d * es)};
 }
-bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+// Whether they have an element in common; two windows of columns of one buffer have none.
+bool meet(Span a, Span b) {
+    if (a.lo == a.hi || b.lo == b.hi || a.hi <= b.lo || b.hi <= a.lo) return false;
+    if (a.row != b.row) return true;
+    const uintptr_t off = (a.lo > b.lo ? a.lo - b.lo : b.lo - a.lo) % a.row;
+    return a.lo > b.lo ? !(off >= b.width && off + a.width <= a.row) : !(off >= a.width && off + b.width <= a.row);
+}
 
 // Sizes shared by the three row operators.
 int check_rows(int32_t dtype, int64_t n, int64_t d, int32_t k, int64_t rows) {

@@ -32,3 +32,38 @@ def test_sort_pairs_of_a_thread(n, k, m, align, capacity):
     source[slot[order[kept]]] = order[kept]
     for got, want in zip(plan, (slot.reshape(n, k), source, counts, offsets)):
         assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,gap", [(64, 0), (101, 3), (2048, 0), (2050, 6)])
+def test_windows_of_one_buffer(d, gap, dtype):
+    """Inputs and outputs side by side in the rows of one buffer have no element in common."""
+    n, k, m = 24, 1, 5
+    r = torch.Generator(device=DEV).manual_seed(d)
+    idx = torch.randint(0, m, (n, k), device=DEV, dtype=torch.int32, generator=r)
+    plan = sk.route_sort(idx, m)
+    w = torch.rand(n, k, device=DEV, generator=r)
+
+    def pair(seed):
+        """Two (n, d) windows of a wide buffer: one with values, the other of sevens; and a check of all the rest."""
+        wide = torch.full((n, 2 * d + gap), 7.0, dtype=DTYPES[dtype], device=DEV)
+        a, b = wide[:, :d], wide[:, d + gap:]
+        a.copy_(torch.randn(n, d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(seed)))
+        return a, b, lambda was: torch.equal(a, was) and bool((wide[:, d:d + gap] == 7.0).all())
+
+    for swap in (False, True):
+        for call in (lambda x, out: sk.route_dispatch(x, plan, w, out=out), lambda x, out: sk.route_combine(x, plan, w, out=out),
+                     lambda x, out: sk.route_combine(x.contiguous(), plan, w, add=x, out=out),
+                     lambda x, out: sk.route_combine_grad(x.contiguous(), plan, w, x, d_rows=out)[0],
+                     lambda x, out: sk.route_combine_grad(x, plan, w, x.contiguous(), d_rows=out)[0]):
+            a, b, same = pair(3)
+            if swap:  # the window with values behind the other
+                values = a.clone()
+                b.copy_(values)
+                a.fill_(7.0)
+                got, want = call(b, a), call(values, torch.empty_like(values))
+                assert torch.equal(got, want) and torch.equal(b, values)
+            else:
+                was = a.clone()
+                got, want = call(a, b), call(was, torch.empty_like(was))
+                assert torch.equal(got, want) and same(was)
