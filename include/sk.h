@@ -590,7 +590,8 @@ int sk_scores_logprobs_grad(const void *scores, int32_t dtype, int64_t n, int64_
  *     ratio (n):   min(1, p_i(x) / q_i(x)) of every drafted token, also behind the stop;
  *                  0 at and behind the request's row without one;
  *     logp (n):    log p_i of the token emitted; 0 where none is.
- * Rows of no request are left as they are.  out_tokens may be tokens.  A drafted token
+ * Rows of no request are left as they are.  out_tokens may be tokens; other outputs must not
+ * overlap an input that is read (SK_ERR_OVERLAP; not checked for the draft's rows).  A drafted token
  * >= m is not taken; a masked one (p = 0) neither; one with q = 0 < p is.  A row that the
  * mask leaves empty takes nothing and draws nothing (-1).  A NaN or +inf score, of the draft
  * too, makes its row's ratio NaN (not taken) and nothing is drawn there.  ratio and logp
@@ -631,7 +632,7 @@ size_t sk_route_sort_workspace_bytes(int64_t n, int32_t k, int64_t m);
  * Choices outside [0, m) are dropped, and with capacity > 0 those of an expert after
  * its first `capacity`.  counts (m): rows of each expert; offsets (m + 1): its first
  * row, a multiple of align >= 1; offsets[m] is the end of the last segment.
- * slot (n, k): the row of each choice, -1: dropped.  source (rows): the choice of each
+ * slot (n, k): the row of each choice, -1: dropped; it may be idx.  source (rows): the choice of each
  * row, -1: none (a segment's padding, and all rows from offsets[m] on); rows >=
  * sk_route_sort_rows(n, k, m, align, capacity).
  */
@@ -665,7 +666,8 @@ int sk_route_combine(const void *in, int32_t dtype, int64_t rows, int64_t d, int
  * Gradient of sk_route_combine from d_y (n, d) (that of add is d_y itself):
  *     d_rows[slot[i, r]] = weights[i, r] d_y[i],  d_weights[i, r] = <in[slot[i, r]], d_y[i]>,
  * 0 for a dropped choice; padding and the rows behind as in sk_route_dispatch.  Either
- * output may be NULL; without d_weights `in` is not read.  d_rows may be `in` (same stride).
+ * output may be NULL; without d_weights `in` is not read.  d_rows may be `in` (same stride), d_weights
+ * may be weights.
  * With in = the gradient of sk_route_dispatch's rows and d_y = x, d_weights is that of its weights.
  */
 int sk_route_combine_grad(const void *in, int32_t dtype, int64_t rows, int64_t d, int64_t ld_in,

@@ -580,22 +580,6 @@ hipError_t combine_grad(RowsArgs A, hipStream_t s) {
     return launch_rows(A, past_caches<T>(A) ? by_lanes(std::true_type()) : by_lanes(std::false_type()), s);
 }
 
-// Rows of d elements, stride ld, at address p.
-struct Span {
-    uintptr_t lo, hi, row, width;  // in bytes: what they span, the stride, a row
-};
-Span span_of(const void* p, int64_t n, int64_t d, int64_t ld, int es) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, n > 0 ? a + (uintptr_t)(((n - 1) * ld + d) * es) : a, (uintptr_t)(ld * es), (uintptr_t)(d * es)};
-}
-// Whether they have an element in common; two windows of columns of one buffer have none.
-bool meet(Span a, Span b) {
-    if (a.lo == a.hi || b.lo == b.hi || a.hi <= b.lo || b.hi <= a.lo) return false;
-    if (a.row != b.row) return true;
-    const uintptr_t off = (a.lo > b.lo ? a.lo - b.lo : b.lo - a.lo) % a.row;
-    return a.lo > b.lo ? !(off >= b.width && off + a.width <= a.row) : !(off >= a.width && off + b.width <= a.row);
-}
-
 // Sizes shared by the three row operators.
 int check_rows(int32_t dtype, int64_t n, int64_t d, int32_t k, int64_t rows) {
     if (dtype != SK_F32 && dtype != SK_BF16 && dtype != SK_F16) return SK_ERR_DTYPE;
@@ -608,6 +592,13 @@ int check_matrix(const void* p, int32_t dtype, int64_t rows, int64_t d, int64_t 
     if (!good_stride(ld, rows, d)) return SK_ERR_SHAPE;
     if (rows > 0 && !p) return SK_ERR_NULL;
     return reinterpret_cast<uintptr_t>(p) % elem_size(dtype) != 0 ? SK_ERR_DTYPE : SK_OK;
+}
+
+// Whether an output meets what a plan and its weights hold.
+bool meet_plan(Span out, const int32_t* slot, const float* weights, int64_t pairs, const int32_t* counts, const int32_t* offsets,
+               int64_t m) {
+    return meet(span_of(slot, pairs, 4), out) || (weights && meet(span_of(weights, pairs, 4), out)) ||
+           (counts && (meet(span_of(counts, m, 4), out) || meet(span_of(offsets, m + 1, 4), out)));
 }
 
 // counts and offsets are given together, with m.
@@ -642,6 +633,10 @@ int sk_route_sort(const int32_t* idx, int64_t n, int32_t k, int64_t m, int32_t a
     if ((n > 0 && (!idx || !slot)) || (rows > 0 && !source) || !counts || !offsets) return SK_ERR_NULL;
     const SortPlan P = sort_plan(n * k, m);
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < P.total) return SK_ERR_WORKSPACE;
+    const Span choices = span_of(idx, n * k, 4);
+    if ((slot != idx && meet(span_of(slot, n * k, 4), choices)) || meet(span_of(source, rows, 4), choices) ||
+        meet(span_of(counts, m, 4), choices) || meet(span_of(offsets, m + 1, 4), choices))
+        return SK_ERR_OVERLAP;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     SortArgs A{};
     A.idx = idx;
@@ -686,7 +681,9 @@ int sk_route_dispatch(const void* x, int32_t dtype, int64_t n, int64_t d, int64_
     if ((st = check_padding(counts, offsets, m))) return st;
     if (n == 0 || rows == 0) return SK_OK;
     if (!slot) return SK_ERR_NULL;
-    if (meet(span_of(x, n, d, ld, elem_size(dtype)), span_of(out, rows, d, ld_out, elem_size(dtype)))) return SK_ERR_OVERLAP;
+    const Span to = span_of(out, rows, d, ld_out, elem_size(dtype));
+    if (meet(span_of(x, n, d, ld, elem_size(dtype)), to) || meet_plan(to, slot, weights, n * k, counts, offsets, m))
+        return SK_ERR_OVERLAP;
     RowsArgs A{};
     A.n = n;
     A.d = (int)d;
@@ -717,7 +714,8 @@ int sk_route_combine(const void* in, int32_t dtype, int64_t rows, int64_t d, int
     if (!slot) return SK_ERR_NULL;
     const int es = elem_size(dtype);
     const Span out = span_of(y, n, d, ld_y, es);
-    if (meet(span_of(in, rows, d, ld_in, es), out)) return SK_ERR_OVERLAP;
+    if (meet(span_of(in, rows, d, ld_in, es), out) || meet_plan(out, slot, weights, n * k, nullptr, nullptr, 0))
+        return SK_ERR_OVERLAP;
     const bool in_place = add == y && (ld_add == ld_y || n == 1);
     if (add && !in_place && meet(span_of(add, n, d, ld_add, es), out)) return SK_ERR_OVERLAP;
     RowsArgs A{};
@@ -756,6 +754,12 @@ int sk_route_combine_grad(const void* in, int32_t dtype, int64_t rows, int64_t d
         if (meet(span_of(d_y, n, d, ld_dy, es), out)) return SK_ERR_OVERLAP;
         const bool in_place = in == d_rows && (ld_in == ld_out || rows == 1);
         if (d_weights && !in_place && meet(span_of(in, rows, d, ld_in, es), out)) return SK_ERR_OVERLAP;
+        if (meet_plan(out, slot, weights, n * k, counts, offsets, m)) return SK_ERR_OVERLAP;
+    }
+    if (d_weights) {
+        const Span out = span_of(d_weights, n * k, 4);
+        if (meet(span_of(in, rows, d, ld_in, es), out) || meet(span_of(d_y, n, d, ld_dy, es), out)) return SK_ERR_OVERLAP;
+        if (meet_plan(out, slot, d_weights == weights ? nullptr : weights, n * k, counts, offsets, m)) return SK_ERR_OVERLAP;
     }
     RowsArgs A{};
     A.n = n;

@@ -331,6 +331,29 @@ inline int check_grad(const void* scores, int64_t ld, const void* grad, int64_t 
     return SK_ERR_OVERLAP;
 }
 
+// Rows of d elements, stride ld, at address p.
+struct Span {
+    uintptr_t lo, hi, row, width;  // in bytes: what they span, the stride (0: a single row), a row
+};
+inline Span span_of(const void* p, int64_t n, int64_t d, int64_t ld, int es) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, n > 0 ? a + (uintptr_t)(((n - 1) * ld + d) * es) : a, n > 1 ? (uintptr_t)(ld * es) : 0, (uintptr_t)(d * es)};
+}
+inline Span span_of(const void* p, int64_t n, int es) { return span_of(p, 1, n, n, es); }
+// Whether they have an element in common; two windows of columns of one buffer have none.
+inline bool meet(Span a, Span b) {
+    if (a.lo == a.hi || b.lo == b.hi || a.hi <= b.lo || b.hi <= a.lo) return false;
+    const uintptr_t row = a.row ? a.row : b.row;
+    if (row == 0 || (b.row && b.row != row)) return true;
+    if (a.lo > b.lo) {
+        const Span c = a;
+        a = b;
+        b = c;
+    }
+    const uintptr_t off = (b.lo - a.lo) % row;
+    return !(off >= a.width && off + b.width <= row);
+}
+
 inline int check_temperature(float eps) {
     if (!std::isfinite(eps) || eps <= 0.0f) return SK_ERR_EPS;
     // log2e / eps, the factor of every exponent, must be finite and nonzero in fp32

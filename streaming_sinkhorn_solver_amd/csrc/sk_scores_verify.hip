@@ -918,6 +918,15 @@ int sk_scores_verify(const void* scores, int32_t dtype, int64_t n, int64_t m, in
     if (b == 0) return SK_OK;
     if (!starts || !accepted || !next || (!greedy && !u_sample)) return SK_ERR_NULL;
     if (n > 0 && (!tokens || !out_tokens || !ratio || !logp || (!greedy && !u_accept))) return SK_ERR_NULL;
+    const int es = elem_size(dtype);
+    // (not the draft's rows: which of them are there is not known here)
+    const Span inputs[] = {span_of(tokens, n, 8), span_of(starts, b + 1, 8), span_of(scores, n, m, ld, es),
+                           span_of(u_accept, greedy ? 0 : n, 4), span_of(u_sample, greedy ? 0 : b, 4)};
+    const Span outputs[] = {span_of(out_tokens, n, 8), span_of(accepted, b, 4), span_of(next, b, 8), span_of(ratio, n, 4),
+                            span_of(logp, n, 4)};
+    for (const Span& in : inputs)
+        for (const Span& out : outputs)
+            if (meet(in, out) && !(&in == inputs && &out == outputs && out_tokens == tokens)) return SK_ERR_OVERLAP;
     char* base = static_cast<char*>(ws);
     VfArgs A{};
     A.s = scores;

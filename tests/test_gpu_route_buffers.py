@@ -67,3 +67,25 @@ def test_windows_of_one_buffer(d, gap, dtype):
                 was = a.clone()
                 got, want = call(a, b), call(was, torch.empty_like(was))
                 assert torch.equal(got, want) and same(was)
+
+
+@pytest.mark.parametrize("d", [5, 40, 200, 700, 5000])
+@pytest.mark.parametrize("n,k", [(1, 2), (333, 19), (4000, 3)])
+def test_outputs_in_place_of_small_inputs(n, k, d):
+    """The slots over the choices, the weights' gradient over the weights."""
+    m, n = 30, min(n, 400) if d > 700 else n
+    r = torch.Generator(device=DEV).manual_seed(n + d)
+    idx = torch.randint(-2, m + 2, (n, k), device=DEV, dtype=torch.int32, generator=r)
+    plan = sk.route_sort(idx, m, align=4)
+    over = idx.clone()
+    got = sk.route_sort(over, m, align=4, out=plan._replace(slot=over, source=plan.source.clone()))
+    assert got.slot.data_ptr() == over.data_ptr() and all(torch.equal(a, b) for a, b in zip(got[:4], plan[:4]))
+    x = torch.randn(n, d, device=DEV, generator=r).bfloat16()
+    rows = torch.randn(plan.source.numel(), d, device=DEV, generator=r).bfloat16()
+    w = torch.randn(n, k, device=DEV, generator=r)
+    want, want_w = sk.route_combine_grad(rows, plan, w, x, d_rows=rows.clone())
+    out = rows.clone()
+    got_w = sk.route_combine_grad(rows, plan, w, x, d_rows=out, d_weights=w)[1]
+    assert got_w is w and torch.equal(w, want_w) and torch.equal(out, want)
+    with pytest.raises(ValueError, match="SK_ERR_OVERLAP"):
+        sk.route_combine_grad(rows, plan, w, x, d_weights=rows.view(-1)[:2 * n * k].view(torch.float32).view(n, k))
