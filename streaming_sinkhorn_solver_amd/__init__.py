@@ -816,7 +816,8 @@ def scores_logprobs_grad(scores, targets: torch.Tensor | None, fwd: Logprobs, *,
 class Verified(NamedTuple):
     """Of each request the number of drafted tokens taken (b,) int32 and the token drawn behind them (b,) int64 (-1:
     none); of each row the token emitted there (n,) int64 (-1: none), min(1, p/q) of its drafted token and the
-    log-probability of the emitted one, (n,) float32 (0: none)."""
+    log-probability of the emitted one, (n,) float32 (0: none).  New ones are slices of two allocations, which live, and
+    are saved, as a whole: clone what is kept for long."""
     accepted: torch.Tensor
     next: torch.Tensor
     tokens: torch.Tensor
@@ -870,8 +871,9 @@ def scores_verify(scores, tokens: torch.Tensor, starts: torch.Tensor, u_accept: 
         # two allocations for all (a call on a few rows is bound by the host); the workspace, first, is aligned by it
         own = 0 if ws is not None else _verify_bytes(s.dtype, n, m, b) // 4
         own_ws, ratio, logp, acc = torch.empty(own + 2 * n + b, dtype=torch.float32, device=dev).split_with_sizes((own, n, n, b))
-        acc = acc.view(torch.int32)
         tok, nxt = torch.empty(n + b, dtype=torch.int64, device=dev).split_with_sizes((n, b))
+        # (.data: a version of its own, so that a change of one in place is none of the others)
+        acc, nxt, logp = acc.view(torch.int32).data, nxt.data, logp.data
         ws_ptr, ws_bytes = own_ws.data_ptr(), 4 * own
     else:
         acc = _out(out.accepted, (b,), torch.int32, dev, "out.accepted")
@@ -893,7 +895,8 @@ def scores_verify(scores, tokens: torch.Tensor, starts: torch.Tensor, u_accept: 
 class RoutePlan(NamedTuple):
     """Where each choice's row lies: slot (n, k) int32, the row of choice (i, r), -1 where it was dropped; source (rows,)
     int32, the choice i * k + r of a row, -1 of none; counts (m,) int32, rows of each expert; offsets (m + 1,) int32, its
-    first row (a multiple of align), the last entry the end of all."""
+    first row (a multiple of align), the last entry the end of all.  New ones are slices of one allocation, which lives,
+    and is saved, as a whole: clone what is kept for long."""
     slot: torch.Tensor
     source: torch.Tensor
     counts: torch.Tensor
@@ -947,7 +950,8 @@ def route_sort(idx: torch.Tensor, m: int, *, align: int = 1, capacity: int = 0, 
         own = 0 if ws is not None else _sort_bytes(n, k, m) // 4
         buf = torch.empty(own + n * k + rows + 2 * m + 1, dtype=torch.int32, device=dev)
         own_ws, slot, source, counts, offsets = buf.split_with_sizes((own, n * k, rows, m, m + 1))
-        slot = slot.view(n, k)
+        # (.data: a version of its own, so that a change of one in place is none of the others)
+        slot, counts, offsets = slot.view(n, k).data, counts.data, offsets.data
         ws_ptr, ws_bytes = own_ws.data_ptr(), 4 * own
     else:
         slot = _out(out.slot, (n, k), torch.int32, dev, "out.slot")

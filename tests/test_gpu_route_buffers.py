@@ -89,3 +89,35 @@ def test_outputs_in_place_of_small_inputs(n, k, d):
     assert got_w is w and torch.equal(w, want_w) and torch.equal(out, want)
     with pytest.raises(ValueError, match="SK_ERR_OVERLAP"):
         sk.route_combine_grad(rows, plan, w, x, d_weights=rows.view(-1)[:2 * n * k].view(torch.float32).view(n, k))
+
+
+def test_outputs_change_apart():
+    """An output that is changed in place is no change of another: what autograd has saved of a plan stays valid."""
+    plan = sk.route_sort(torch.randint(0, 4, (10, 2), dtype=torch.int32, device=DEV), 4)
+    s = torch.randn(3, 40, device=DEV)
+    v = sk.scores_verify(s, torch.tensor([1, 2, -1], device=DEV), torch.tensor([0, 3], device=DEV), torch.rand(3, device=DEV),
+                         torch.rand(1, device=DEV))
+    for outs in (plan[:4], v):
+        for t in outs:
+            before, values = [o._version for o in outs], [o.clone() for o in outs]
+            t.add_(1)
+            for o, b, x in zip(outs, before, values):
+                assert (o._version != b) == (o is t) and torch.equal(o, x + 1 if o is t else x)
+
+    class Way(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, plan):
+            ctx.save_for_backward(plan.slot, plan.source)
+            return sk.route_dispatch(x, plan)
+
+        @staticmethod
+        def backward(ctx, d_rows):
+            slot, source = ctx.saved_tensors
+            return sk.route_combine(d_rows, sk.RoutePlan(slot, source, None, None)), None
+
+    x = torch.randn(10, 8, device=DEV, requires_grad=True)
+    plan = sk.route_sort(torch.randint(0, 4, (10, 2), dtype=torch.int32, device=DEV), 4)
+    y = Way.apply(x, plan)
+    plan.counts.add_(plan.counts.clone())  # (a sum over training steps)
+    y.backward(torch.ones_like(y))
+    assert (x.grad == 2.0).all()
