@@ -851,8 +851,9 @@ def scores_verify(scores, tokens: torch.Tensor, starts: torch.Tensor, u_accept: 
     where it stops it draws from max(p - q, 0), or from p where no token was drafted, by u_sample (b,): the first column
     whose cumulative weight exceeds u_sample of the whole.  The emitted tokens are then distributed as p.  u_accept (n,)
     and u_sample are float32 from [0, 1); eps = 0 is greedy (the largest score, the first of equal ones, has p = 1) and
-    needs neither.  Decisions and draws are made in float64.  ``out``: a Verified of earlier buffers to write into; its
-    tokens may be the tokens given."""
+    needs neither.  Decisions and draws are made in float64; ratio and logp come from float32 sums, some 1e-7 of p / q
+    and of p.  All requests have the same eps and eps_draft: scores of other temperatures are scaled before, or go in
+    calls of their own.  ``out``: a Verified of earlier buffers to write into; its tokens may be the tokens given."""
     s, code, n, m, ld = _scores(scores)
     dev = s.device
     if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:

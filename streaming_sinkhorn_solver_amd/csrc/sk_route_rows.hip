@@ -22,13 +22,15 @@ constexpr int kRowsMaxTop = 64;
 // equal expert find one another by one ballot per bit of its number, so a pair's rank
 // among the wave's pairs of its expert is a count of lower lanes beside the wave's own
 // counter in LDS.  Adding the counts of the waves and workgroups before gives the rank
-// among all.  131072 choices among 256 take 10.5 us: two launches, the second (7.5) bound
-// by its instructions, 560 in each of a workgroup's 16 waves.
+// among all.  131072 choices among 256 take 10.6 us: two launches of 128 workgroups.  The second
+// (8.0) issues vector instructions in 56 % of its CUs' cycles, 570 in each wave, and its waves
+// wait for the tables' loads and for one another in 58 % of theirs.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortMost = 16;      // pairs per thread at most: a wave's counter fits 16 bits
 constexpr int kSortOne = 4096;     // pairs that one workgroup takes alone
 // Workgroups whose counts the others add up themselves: 64, and up to 256 where that is no more than 32768 counts
-// (524288 choices among 256: 128 take 15.1 us, 64 18.4; 131072 among 1024: 64 take 14.9, 128 18.0, 32 15.4).
+// (524288 choices among 128: 256 take 12.8 us, 128 13.5; among 256: 128 take 15.1, 64 18.3, 256 15.5; among 512: 64 take
+// 20.4, 128 18.1, where 131072 take 12.1 and 13.1; 131072 among 1024: 64 take 14.9, 128 18.0, 32 15.4).
 int sort_groups(int64_t m) { return (int)std::min<int64_t>(256, std::max<int64_t>(64, 32768 / m)); }
 
 struct SortArgs {
@@ -515,14 +517,18 @@ bool whole_lines(const void* p, int64_t ld, int d) {
 
 // Whether the rows that are summed are read past the caches: where no two share a line, or where rows are so long that few
 // of their lines are shared.  65536 x 8 rows of 203 bf16: the sum takes 49 us through the caches and 61 past them, 16384 x 8 of
-// 2040 122 and 107; both gradients of 300 286 and 315, of 2040 362 and 330.
+// 2040 122 and 107; both gradients of 300 286 and 315, of 2040 362 and 330.  Between them, 32768 x 8 rows: the sum of 600 89
+// and 88, of 1010 124 and 110, of 1040 152 and 149, of 1500 184 and 172; both gradients of 600 245 and 232, of 1010 393 and 377, of 1040
+// 409 and 402, of 1500 557 and 591.
 template <class T>
 bool past_caches(const RowsArgs& A) {
     return A.pieces > 128 || whole_lines<T>(A.in, A.ld_in, A.d);
 }
 
 // Few tokens with long rows: several workgroups for each, every one with a run of pieces (1 x 8 rows of 8192 bf16: the sum
-// takes 4.7 us so, 10.5 in one workgroup).
+// takes 4.7 us so, 10.5 in one workgroup; 64 x 8 6.9 and 22.4, dispatch with its sort 8.3 and 13.2; 512 x 8 of 4096 10.4 and 15.4, dispatch
+// 14.5 and 14.3, of 8192 19.3 and 28.2, 20.5 and 21.5).  Of more tokens only the sum would gain (768 x 8 of 4096 12.9 in halves and 17.3, 1024
+// 18.9 and 19.0; dispatch 17.4 and 17.0, 20.9 and 20.1).  The gradient's rows are not shared out: partial dot products would have to be joined.
 void split_rows(RowsArgs& A) {
     const int most = (A.pieces + kBlock - 1) / kBlock;
     if (A.lanes < kBlock || A.n > 512 || most < 2) return;

@@ -664,7 +664,7 @@ __device__ bool draw(const VfArgs& A, int64_t r, Draw d, bool exact, double& rho
 
 // Where each request stops and the sums of the chunks of what it draws from: a wave per chunk, A.parts workgroups per
 // request; one that has all the chunks (ALONE) draws too.  Bound by the issue of some 40 float64 instructions per entry: 64
-// requests over 131072 columns take 22 us, 5 of them to look where each stops.
+// requests over 131072 columns take 21 us, 5 of them to look where each stops.
 template <class T, bool ALONE>
 __global__ __launch_bounds__(kBlock, 4) void k_verify_chunks(VfArgs A) {
     __shared__ Look L;
@@ -694,7 +694,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_verify_chunks(VfArgs A) {
     }
 }
 
-// Bound by the latency of its loads and of three sums over the workgroup: 6 us for one request, 8 for 64.
+// Bound by the latency of its loads and of three sums over the workgroup: 7 us for one request, 9 for 64.
 template <class T>
 __global__ __launch_bounds__(kBlock) void k_verify_draw(VfArgs A) {
     __shared__ Pick P;

@@ -164,7 +164,8 @@ def test_rows(d, dtype):
         close(d_rows, want, 0.0 if weights is None else product_tol(want, dtype), "d_rows")
         assert untouched(buf, d_rows, 7.0)
         _, size = oro.combine_grad(np.abs(gs), slot, offsets, weights, np.abs(xs), np.zeros((rows, d)))
-        # a lane adds the elements of every 16th run at least (8 to a run), then 16 or 256 lanes are added
+        # 8 to 256 lanes, as many as the row's runs where they are fewer (128 count as 64): a lane adds d / 16 elements at most but for
+        # rows of fewer than 20, then the lanes are added
         close(d_w, want_w, (d / 16 + 20) * U * size, "d_weights")
 
 

@@ -63,7 +63,7 @@ def run(data, ref, eps=1.0, eps_draft=1.0, **how):
     return got
 
 
-# one column; around a run of 16 bytes, a wave's row (512 runs), a chunk of the draw (2048), a part of a cut row
+# one column; around a run of 16 bytes, a wave's row (512 runs), four chunks of the draw (512 entries at these sizes), a part of a cut row
 COLUMNS = [1, 2, 5, 8, 33, 511, 2047, 2048, 2049, 4096, 4099, 8192, 8200, 50001, 131072]
 
 
