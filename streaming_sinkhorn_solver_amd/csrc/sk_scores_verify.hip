@@ -413,7 +413,6 @@ __device__ __forceinline__ void chunk_sums(const VfArgs& A, const Draw& d, doubl
         hot = fma(b, over, hot);
         gap = fmin(gap, fma(-near, b, fabs(w)));
     };
-    auto add_one = [&](float x, int j) { e += j == d.out ? 0.0 : exp_near(x, d.ref_p, A.c, A.floor); };
     const int whole = size / (64 * VE) * (64 * VE);  // entries in whole runs of all lanes
     // (the loops are not unrolled: a wave has few chunks, and cold code takes longer to fetch than to run)
     if (d.with_q) {
@@ -432,6 +431,9 @@ __device__ __forceinline__ void chunk_sums(const VfArgs& A, const Draw& d, doubl
 #pragma unroll 1
         for (int j = whole + lane; j < size; j += 64) add_both(T::to(s[j - lane * VE]), T::to(q[j - lane * VE]));
     } else {
+        double floor = A.floor;
+        asm("" : "+v"(floor));  // (in vector registers, where the comparison takes it as it is: 17 us against 18 for 64 rows of 131072)
+        auto add_one = [&](float x, int j) { e += j == d.out ? 0.0 : exp_near(x, d.ref_p, A.c, floor); };
         Run16<T> a, a1;
         if (whole > 0) a1.get(s);
 #pragma unroll 1
